@@ -23,6 +23,12 @@ Entry points (same names as the C ABI):
                                 layer_idx, scales_granularity_mnk=(1, 128, 128),
                                 kv_scales=None, quantization_granularity=0)
     kv_matmul_ragged_paged_scale(... the same, weight = [W_k | W_v] ...)
+    tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_lengths,
+                        new_lengths, free_pages, free_count, page_size)
+    attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, page_table,
+                           layer_idx, scale, workspace, causal=True, window=0,
+                           kv_scales=None, quantization_granularity=0)
+    attention_ragged_paged_workspace(T, batch, num_q_heads, num_kv_heads, head_dim)
 Each returns None on success and raises QgError carrying the status otherwise.
 Measurement yardsticks (include/qgemm_probe.h): read_contiguous, read_strips, mfma_loop,
 empty_launch.
@@ -36,7 +42,8 @@ import torch
 
 __all__ = ["load", "QgError", "qgemm_w4", "qgemm_w4_nk", "qgemm_w4_epilogue", "grouped_gemm", "grouped_gemm_w4",
            "grouped_gemm_epilogue", "grouped_gemm_w4_epilogue",
-           "k_matmul_ragged_paged_scale", "kv_matmul_ragged_paged_scale", "status_string", "LIB_PATH", "QG", "EPI_BIAS", "EPI_RESIDUAL",
+           "k_matmul_ragged_paged_scale", "kv_matmul_ragged_paged_scale",
+           "tables_ragged_paged", "attention_ragged_paged", "attention_ragged_paged_workspace", "status_string", "LIB_PATH", "QG", "EPI_BIAS", "EPI_RESIDUAL",
            "EPI_SILU_GATE"]
 
 # qgemm_w4_epilogue flags
@@ -112,6 +119,13 @@ def load(path: str | None = None):
     lib.k_matmul_ragged_paged_scale.restype = ctypes.c_int
     lib.kv_matmul_ragged_paged_scale.argtypes = lib.k_matmul_ragged_paged_scale.argtypes
     lib.kv_matmul_ragged_paged_scale.restype = ctypes.c_int
+    lib.tables_ragged_paged.argtypes = [T, T, T, T, T, T, T, T, ctypes.c_int32, ctypes.c_void_p]
+    lib.tables_ragged_paged.restype = ctypes.c_int
+    lib.attention_ragged_paged.argtypes = [T, T, T, ctypes.POINTER(QgPagedKV), ctypes.c_uint32, ctypes.c_float,
+                                           ctypes.c_int32, ctypes.c_int32, T, ctypes.c_void_p]
+    lib.attention_ragged_paged.restype = ctypes.c_int
+    lib.attention_ragged_paged_workspace.argtypes = [ctypes.c_int64] * 5
+    lib.attention_ragged_paged_workspace.restype = ctypes.c_int64
     lib.qg_status_string.argtypes = [ctypes.c_int]
     lib.qg_status_string.restype = ctypes.c_char_p
     lib.qg_version.argtypes = []
@@ -328,6 +342,78 @@ def kv_matmul_ragged_paged_scale(hidden, input_row_offsets, weight, input_scale,
     return _kv_call(load().kv_matmul_ragged_paged_scale, hidden, input_row_offsets, weight, input_scale,
                     weight_scale, kv_blocks, cache_lengths, page_table, layer_idx, scales_granularity_mnk,
                     kv_scales, quantization_granularity, stream, raise_on_error)
+
+
+def _device_of(tensors):
+    """The GPU that all of a call's tensors are on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the library must be on a GPU")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("tensors of one call must be on one GPU")
+    return dev
+
+
+def _on(dev, stream, call):
+    """call(stream) with the tensors' GPU as the current one; the default stream is
+    that GPU's current stream."""
+    if dev is None or dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages,
+                        free_count, page_size: int, stream=None, raise_on_error: bool = True) -> int:
+    """Row offsets [B + 1], new page table entries (page_table [B, W], updated) and slot map
+    [T] (or None) of one step, from cache_lengths and new_lengths [B] and a stack of free
+    pages (free_pages [F], free_count [1]). result [2]: pages left, status (0: built; else
+    1 too few pages | 2 a sequence past W pages | 4 more tokens than slots, nothing written)."""
+    lib = load()
+    tables = (input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages, free_count)
+    dev = _device_of(tables)
+    d = [None if t is None else ctypes.byref(describe(t, QG.I32 if i == 1 and t.dtype == torch.int32 else _u32(t)))
+         for i, t in enumerate(tables)]
+    st = _on(dev, stream, lambda s: lib.tables_ragged_paged(*d, int(page_size), s))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def attention_ragged_paged_workspace(T: int, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """float32 elements of workspace for attention_ragged_paged calls of these sizes."""
+    return load().attention_ragged_paged_workspace(int(T), int(batch), int(num_q_heads), int(num_kv_heads),
+                                                   int(head_dim))
+
+
+def attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, page_table, layer_idx: int,
+                           scale: float, workspace, causal: bool = True, window: int = 0, kv_scales=None,
+                           quantization_granularity: int = 0, stream=None, raise_on_error: bool = True) -> int:
+    """out [T, Hq, D] = attention of the new tokens' queries q [T, Hq, D] (bf16, ragged by
+    input_row_offsets) over layer `layer_idx` of the paged cache `kv_blocks`
+    [L, 2, P, S, Hkv, D] (bf16, or e4m3 codes held in float8_e4m3fn / uint8 with f32
+    `kv_scales`), which holds the new tokens' keys and values already. workspace: a float32
+    tensor of attention_ragged_paged_workspace(...) elements."""
+    lib = load()
+    dev = _device_of((out, q, input_row_offsets, kv_blocks, cache_lengths, page_table, kv_scales, workspace))
+    batch = input_row_offsets.shape[0] - 1 if input_row_offsets is not None and input_row_offsets.dim() == 1 else 0
+    for t, shape in ((cache_lengths, (batch,)), (page_table, (batch, page_table.shape[-1] if page_table is not None and page_table.dim() else 0))):
+        if t is not None and (t.dtype not in (torch.int32, torch.uint32) or tuple(t.shape) != shape
+                              or not t.is_contiguous()):
+            raise ValueError("cache_lengths [B] and page_table [B, max_pages] must be contiguous int32 or uint32 tensors")
+    kv = _paged_kv(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity)
+    st = _on(dev, stream, lambda s: lib.attention_ragged_paged(
+        ctypes.byref(describe(out)), ctypes.byref(describe(q)),
+        ctypes.byref(describe(input_row_offsets, _u32(input_row_offsets))), ctypes.byref(kv), int(layer_idx),
+        float(scale), int(bool(causal)), int(window), ctypes.byref(describe(workspace)), s))
+    if raise_on_error:
+        _check(st)
+    return st
 
 
 def read_contiguous(src: torch.Tensor, sink: torch.Tensor, workgroups: int = 512, stream=None,

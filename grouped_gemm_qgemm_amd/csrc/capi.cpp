@@ -1,6 +1,7 @@
 // C ABI entry points: host-side argument checks, launch-shape choice and
 // launch. Every check runs before the first HIP call, so a rejected call
 // enqueues nothing and touches no output.
+#include <cmath>
 #include <mutex>
 
 #include <hip/hip_runtime.h>
@@ -299,6 +300,21 @@ qg_status grouped_gemm_w4_epilogue(const qg_tensor* c, const qg_tensor* a, const
                               pack_factor, epilogue, bias, residual, stream);
 }
 
+// Granularity and scales of an e4m3 cache.
+static qg_status check_cache_scales(const qg_paged_kv* kv) {
+  const int64_t* bs = kv->blocks.shape;
+  const int64_t G = kv->quantization_granularity;
+  if (G != 32 && G != 64 && G != 128) return QG_ERR_UNSUPPORTED;
+  if (bs[5] % G != 0) return QG_ERR_UNSUPPORTED;
+  if (kv->scales.rank != 6) return QG_ERR_RANK;
+  const qg_status st = check_tensor(&kv->scales, 6, QG_F32);
+  if (st != QG_OK) return st;
+  const int64_t* ss = kv->scales.shape;
+  for (int i = 0; i < 5; ++i)
+    if (ss[i] != bs[i]) return QG_ERR_SHAPE;
+  return ss[5] == bs[5] / G ? QG_OK : QG_ERR_SHAPE;
+}
+
 // planes: 1 (keys only) or 2 (weight columns = [W_k | W_v])
 static qg_status kv_proj_impl(const qg_tensor* hidden, const qg_tensor* input_row_offsets,
                               const qg_tensor* weight, const qg_tensor* input_scale,
@@ -333,16 +349,8 @@ static qg_status kv_proj_impl(const qg_tensor* hidden, const qg_tensor* input_ro
   if (weight_scale->shape[0] != Kh / 128 || weight_scale->shape[1] != N / 128) return QG_ERR_SHAPE;
   if (bs[1] != 2 || Hkv * D * planes != N) return QG_ERR_SHAPE;
   if (planes > 1 && (Hkv * D) % 128 != 0) return QG_ERR_SHAPE;   // each 128-column tile in one plane
-  int64_t G = 0;
-  if (fp8) {
-    G = kv->quantization_granularity;
-    if (G != 32 && G != 64 && G != 128) return QG_ERR_UNSUPPORTED;
-    if (D % G != 0) return QG_ERR_UNSUPPORTED;
-    if (kv->scales.rank != 6) return QG_ERR_RANK;
-    if ((st = check_tensor(&kv->scales, 6, QG_F32)) != QG_OK) return st;
-    const int64_t* ss = kv->scales.shape;
-    if (ss[0] != L || ss[1] != 2 || ss[2] != P || ss[3] != S || ss[4] != Hkv || ss[5] != D / G) return QG_ERR_SHAPE;
-  }
+  const int64_t G = fp8 ? kv->quantization_granularity : 0;
+  if (fp8 && (st = check_cache_scales(kv)) != QG_OK) return st;
   if ((int64_t)layer_idx >= L) return QG_ERR_INVALID_ARG;
   if (kv->max_pages_per_seq <= 0 && T > 0) return QG_ERR_INVALID_ARG;
   if (B > 0 && T > 0 && (!kv->cache_lengths || !kv->page_table)) return QG_ERR_NULL;
@@ -383,6 +391,109 @@ qg_status kv_matmul_ragged_paged_scale(const qg_tensor* hidden, const qg_tensor*
                                        hipStream_t stream) {
   return kv_proj_impl(hidden, input_row_offsets, weight, input_scale, weight_scale, scales_granularity_mnk, kv,
                       layer_idx, 2, stream);
+}
+
+qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tensor* slot_map,
+                              const qg_tensor* page_table, const qg_tensor* result,
+                              const qg_tensor* cache_lengths, const qg_tensor* new_lengths,
+                              const qg_tensor* free_pages, const qg_tensor* free_count, int32_t page_size,
+                              hipStream_t stream) {
+  if (!input_row_offsets || !page_table || !result || !cache_lengths || !new_lengths || !free_pages || !free_count)
+    return QG_ERR_NULL;
+  qg_status st;
+  if ((st = check_tensor(input_row_offsets, 1, QG_U32)) != QG_OK) return st;
+  if (slot_map && (st = check_tensor(slot_map, 1, QG_I32)) != QG_OK) return st;
+  if ((st = check_tensor(page_table, 2, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(result, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(cache_lengths, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(new_lengths, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(free_pages, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(free_count, 1, QG_U32)) != QG_OK) return st;
+  const int64_t B = cache_lengths->shape[0], W = page_table->shape[1];
+  if (new_lengths->shape[0] != B || page_table->shape[0] != B || input_row_offsets->shape[0] != B + 1)
+    return QG_ERR_SHAPE;
+  if (result->shape[0] != 2 || free_count->shape[0] != 1) return QG_ERR_SHAPE;
+  if (page_size <= 0) return QG_ERR_INVALID_ARG;
+  const int64_t F = free_pages->shape[0], T = slot_map ? slot_map->shape[0] : 0;
+  if (B > qg::kTablesMaxBatch || W > INT32_MAX / page_size || F > INT32_MAX || T > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (B == 0) return QG_OK;
+  // a slot map without elements still bounds the number of tokens
+  static int32_t none;
+  qg::TablesArgs p{static_cast<uint32_t*>(input_row_offsets->data),
+                   !slot_map ? nullptr : T > 0 ? static_cast<int32_t*>(slot_map->data) : &none,
+                   static_cast<uint32_t*>(page_table->data), static_cast<uint32_t*>(result->data),
+                   static_cast<const uint32_t*>(cache_lengths->data), static_cast<const uint32_t*>(new_lengths->data),
+                   static_cast<const uint32_t*>(free_pages->data), static_cast<const uint32_t*>(free_count->data),
+                   (int)B, (int)W, F, T, page_size, device_cus()};
+  return launch_status(qg::launch_tables_ragged(p, stream));
+}
+
+int64_t attention_ragged_paged_workspace(int64_t T, int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
+                                         int64_t head_dim) {
+  if (T <= 0 || batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
+  return qg::attention_paged_workspace(T, batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                 const qg_paged_kv* kv, uint32_t layer_idx, float scale, int32_t causal,
+                                 int32_t window, const qg_tensor* workspace, hipStream_t stream) {
+  if (!out || !q || !input_row_offsets || !kv || !workspace) return QG_ERR_NULL;
+  if (out->rank != 3 || q->rank != 3 || input_row_offsets->rank != 1 || kv->blocks.rank != 6 || workspace->rank != 1)
+    return QG_ERR_RANK;
+  qg_status st;
+  if ((st = check_tensor(out, 3, QG_BF16)) != QG_OK) return st;
+  if ((st = check_tensor(q, 3, QG_BF16)) != QG_OK) return st;
+  if ((st = check_tensor(input_row_offsets, 1, QG_U32)) != QG_OK) return st;
+  const bool fp8 = kv->blocks.dtype == QG_FP8_E4M3;   // quantized cache
+  if ((st = check_tensor(&kv->blocks, 6, fp8 ? QG_FP8_E4M3 : QG_BF16)) != QG_OK) return st;
+  if ((st = check_tensor(workspace, 1, QG_F32)) != QG_OK) return st;
+  const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
+  const int64_t B = input_row_offsets->shape[0] - 1;
+  const int64_t* bs = kv->blocks.shape;
+  const int64_t L = bs[0], P = bs[2], S = bs[3], Hkv = bs[4];
+  if (B < 0 || out->shape[0] != T || out->shape[1] != Hq || out->shape[2] != D) return QG_ERR_SHAPE;
+  if (bs[1] != 2 || bs[5] != D) return QG_ERR_SHAPE;
+  if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return QG_ERR_SHAPE;
+  if (D % 8 != 0) return QG_ERR_ALIGN;
+  if (fp8 && (st = check_cache_scales(kv)) != QG_OK) return st;
+  if ((int64_t)layer_idx >= L) return QG_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0) return QG_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return QG_ERR_UNSUPPORTED;
+  if (D > 256) return QG_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0 || Hq == 0 || D == 0) return QG_OK;
+  if (P == 0 || S == 0 || kv->max_pages_per_seq <= 0) return QG_ERR_INVALID_ARG;
+  if (!kv->cache_lengths || !kv->page_table) return QG_ERR_NULL;
+  if (workspace->shape[0] < qg::attention_paged_workspace(T, B, Hq, Hkv, D)) return QG_ERR_SHAPE;
+  // rows of a key/value head and positions of a sequence are counted in 32 bits
+  if (B > INT32_MAX / 2 || S > INT32_MAX / 2 || Hq > INT32_MAX / 2 || T > (INT32_MAX / 2) / (Hq / Hkv) ||
+      kv->max_pages_per_seq > (INT32_MAX / 2) / S)
+    return QG_ERR_UNSUPPORTED;
+  qg::AttnArgs p{};
+  p.out = static_cast<uint16_t*>(out->data);
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.offs = static_cast<const uint32_t*>(input_row_offsets->data);
+  p.blocks = kv->blocks.data;
+  p.scales = fp8 ? static_cast<const float*>(kv->scales.data) : nullptr;
+  p.cache_len = kv->cache_lengths;
+  p.page_table = kv->page_table;
+  p.workspace = static_cast<float*>(workspace->data);
+  p.T = T;
+  p.max_pages = kv->max_pages_per_seq;
+  p.pages = P;
+  p.batch = (int)B;
+  p.hq = (int)Hq;
+  p.hkv = (int)Hkv;
+  p.group = (int)(Hq / Hkv);
+  p.d = (int)D;
+  p.page_size = (int)S;
+  p.layer = (int)layer_idx;
+  p.gran = fp8 ? (int)kv->quantization_granularity : 0;
+  p.causal = causal ? 1 : 0;
+  p.window = window;
+  p.fp8 = fp8 ? 1 : 0;
+  p.num_cus = device_cus();
+  p.scale = scale;
+  return launch_status(qg::launch_attention_paged(p, stream));
 }
 
 }  // extern "C"

@@ -89,6 +89,38 @@ struct KProjArgs {
   int hidden_fp8 = 0;            // hidden is e4m3 [T, Kh] (then `hidden` points at bytes)
 };
 
+// Tables of the paged cache (tables_ragged_paged).
+constexpr int kTablesMaxBatch = 8192;   // two prefix sums in 64 KB of LDS
+struct TablesArgs {
+  uint32_t* offsets;           // [batch + 1]
+  int32_t* slots;              // [slot_len] or NULL
+  uint32_t* table;             // [batch, max_pages]
+  uint32_t* result;            // [2]
+  const uint32_t* cached;      // [batch]
+  const uint32_t* fresh;       // [batch]
+  const uint32_t* free_pages;  // [free_len]
+  const uint32_t* free_count;  // [1]
+  int batch, max_pages;
+  int64_t free_len, slot_len;
+  int page_size;
+  int num_cus;
+};
+
+// Attention over the paged cache (attention_ragged_paged).
+struct AttnArgs {
+  uint16_t* out;               // bf16 [T, Hq, D]
+  const uint16_t* q;           // bf16 [T, Hq, D]
+  const uint32_t* offs;        // [batch + 1]
+  const void* blocks;          // bf16 or e4m3 [L, 2, P, S, Hkv, D]
+  const float* scales;         // e4m3: [L, 2, P, S, Hkv, D / gran]
+  const uint32_t* cache_len;   // [batch]
+  const uint32_t* page_table;  // [batch, max_pages]
+  float* workspace;
+  int64_t T, max_pages, pages;
+  int batch, hq, hkv, group, d, page_size, layer, gran, causal, window, fp8, num_cus;
+  float scale;
+};
+
 // Decode-shaped W4A16 (M <= 16).
 hipError_t launch_w4_decode(const W4Args& p, hipStream_t stream);
 
@@ -101,5 +133,12 @@ hipError_t launch_grouped_bf16(const GroupedArgs& p, hipStream_t stream);
 hipError_t launch_w4_grouped(const W4GroupedArgs& p, hipStream_t stream);
 
 hipError_t launch_kproj_fp8(const KProjArgs& p, hipStream_t stream);
+
+hipError_t launch_tables_ragged(const TablesArgs& p, hipStream_t stream);
+
+hipError_t launch_attention_paged(const AttnArgs& p, hipStream_t stream);
+
+// f32 elements of workspace that a call of these sizes may use.
+int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t hkv, int64_t d);
 
 }  // namespace qg

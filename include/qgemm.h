@@ -16,6 +16,12 @@
  *   grouped_gemm_w4              the routing of grouped_gemm over experts stored in
  *                                qgemm_w4's packed 4-bit format
  *
+ * and two operations around the paged KV cache that the projections fill:
+ *
+ *   tables_ragged_paged          row offsets, page table entries and slot map of a step,
+ *                                from the sequences' lengths
+ *   attention_ragged_paged       attention of the new tokens over the cache's pages
+ *
  * Conventions shared by every entry point
  *   - Tensor data pointers are DEVICE pointers unless a comment says "host".
  *     Every tensor is dense, row-major (last dimension contiguous), and its base
@@ -349,6 +355,86 @@ qg_status kv_matmul_ragged_paged_scale(const qg_tensor* hidden, const qg_tensor*
                                        const int32_t* scales_granularity_mnk,
                                        const qg_paged_kv* kv, uint32_t layer_idx,
                                        hipStream_t stream);
+
+/*
+ * tables_ragged_paged - the tables of one step over a paged cache, built on the
+ * device from the sequences' lengths
+ *
+ * Writes what k_matmul_ragged_paged_scale, kv_matmul_ragged_paged_scale and
+ * attention_ragged_paged take as given, so that a step needs no host round trip
+ * (and can be captured and replayed). With c_b = cache_lengths[b] tokens cached,
+ * n_b = new_lengths[b] to be added and S = page_size:
+ *
+ *   input_row_offsets u32 [B + 1]  0, n_0, n_0 + n_1, ...
+ *   page_table        u32 [B, W]   updated: entries ceil(c_b / S) .. ceil((c_b + n_b) / S) - 1
+ *                                  of sequence b receive pages of the free stack, in order of
+ *                                  b and then of the entry; every other entry is left as it was
+ *   slot_map          i32 [T]      or NULL: element input_row_offsets[b] + j becomes
+ *                                  page * S + slot of position c_b + j (the row of a layer's
+ *                                  plane, [P * S, Hkv, D]); elements behind the last token are
+ *                                  left as they were
+ *   result            u32 [2]      [0]: pages left on the free stack, [1]: status (below)
+ *   cache_lengths, new_lengths u32 [B]   a sequence with n_b = 0 is left alone, whatever c_b
+ *   free_pages        u32 [F]      a stack of free page ids: the top is element free_count[0] - 1
+ *   free_count        u32 [1]      pages on it (result[0] of one call may be free_count of the
+ *                                  next: a view of its first element, in another buffer)
+ *
+ * result[1] is 0 when the tables were built, else the OR of
+ *   1  the stack holds too few pages (or free_count[0] > F)
+ *   2  a sequence with new tokens is longer than W * S
+ *   4  there are more tokens than slot_map has elements (2^31 - 1 without one)
+ * and then nothing but `result` is written, with result[0] = free_count[0]: the
+ * caller looks at it before the tables are used. Page ids are not checked; they
+ * are below 2^31 / S. cache_lengths is not updated. B above 8192, or W * S above
+ * 2^31 - 1, is QG_ERR_UNSUPPORTED; B = 0 is a no-op.
+ */
+qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tensor* slot_map,
+                              const qg_tensor* page_table, const qg_tensor* result,
+                              const qg_tensor* cache_lengths, const qg_tensor* new_lengths,
+                              const qg_tensor* free_pages, const qg_tensor* free_count, int32_t page_size,
+                              hipStream_t stream);
+
+/*
+ * attention_ragged_paged - attention of each sequence's new tokens over its pages
+ * of a paged cache: prompts, chunks of prompts, drafted tokens and single tokens
+ * alike, in one ragged call
+ *
+ * Token j of sequence b (row input_row_offsets[b] + j of q) is at position
+ * p = cache_lengths[b] + j; its own key and value are in the cache already (the
+ * projections above write them). Query head h reads key/value head
+ * h / (Hq / Hkv). Over the positions i that the token sees,
+ *
+ *   out[row][h] = sum_i softmax_i(scale * q[row][h] . k_i) v_i
+ *
+ *   out               bf16 [T, Hq, D]
+ *   q                 bf16 [T, Hq, D], Hq a multiple of Hkv (QG_ERR_SHAPE)
+ *   input_row_offsets u32  [B + 1]   offs[0] = 0, non-decreasing, offs[B] <= T: rows from
+ *                                    offs[B] on are left as they were
+ *   kv                the paged cache (bf16, or e4m3 codes with their scales), read only
+ *   layer_idx         < L (QG_ERR_INVALID_ARG otherwise)
+ *   scale             finite and > 0 (QG_ERR_INVALID_ARG otherwise)
+ *   causal            nonzero: positions 0 .. p; 0: 0 .. cache_lengths[b] + n_b - 1, the whole
+ *                     sequence with all its new tokens
+ *   window            0, or the number of positions a token sees, itself included
+ *                     (p - window + 1 .. p); only with causal (QG_ERR_UNSUPPORTED otherwise)
+ *   workspace         f32 [>= attention_ragged_paged_workspace(T, B, Hq, Hkv, D)]
+ *                     (QG_ERR_SHAPE when smaller). Its content before and after a call has no
+ *                     meaning; calls that may run at the same time each need their own
+ *
+ * D is a multiple of 8 (QG_ERR_ALIGN), at most 256 (QG_ERR_UNSUPPORTED). Every
+ * token sees itself, so no row is empty. What a row must not see does not reach
+ * it, infinities and NaN included; pages (page table entries) that no token of
+ * the call sees are not read. Scores, softmax statistics and sums are fp32; the
+ * probabilities are rounded to bf16 for their product with the values, and the
+ * result to bf16 (nearest-even). The result does not depend on timing: the same
+ * call gives the same bits. Offsets, lengths and page ids are not re-validated on
+ * the device.
+ */
+int64_t attention_ragged_paged_workspace(int64_t T, int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
+                                         int64_t head_dim);
+qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                 const qg_paged_kv* kv, uint32_t layer_idx, float scale, int32_t causal,
+                                 int32_t window, const qg_tensor* workspace, hipStream_t stream);
 
 /* Static, never-NULL text for a status code. */
 const char* qg_status_string(qg_status s);

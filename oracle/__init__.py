@@ -24,6 +24,7 @@ from .grouped import grouped_gemm
 from .grouped_w4 import grouped_gemm_w4
 from .kproj import (k_matmul_ragged_paged_scale, kv_matmul_ragged_paged_scale, kproj_exact, kproj_rows,
                     quantize_runs, token_slots)
+from .attention import attention_ragged_paged, cache_rows, tables_ragged_paged
 
 __all__ = [
     "round_to_f16", "round_to_bf16", "round_to", "decode_f16", "decode_bf16", "decode_e4m3",
@@ -31,5 +32,5 @@ __all__ = [
     "dequant_w4", "qgemm_w4", "qgemm_w4_nk", "qgemm_w4_epilogue", "silu", "EPI_BIAS", "EPI_RESIDUAL", "EPI_SILU_GATE",
     "grouped_gemm", "grouped_gemm_w4", "k_matmul_ragged_paged_scale", "kv_matmul_ragged_paged_scale",
     "kproj_exact", "kproj_rows", "quantize_runs",
-    "token_slots",
+    "token_slots", "attention_ragged_paged", "cache_rows", "tables_ragged_paged",
 ]

@@ -285,3 +285,57 @@ def kproj_inputs(seed: int = 5, batch: int = 8, max_len: int = 1024, Kh: int = 4
                        weight_scale=ws, blocks=blocks, cache_lengths=cache_lengths,
                        page_table=page_table, layer_idx=layer_idx, scales=scales,
                        qgran=qgran if cache == "fp8" else 0)
+
+
+# ---------------------------------------------------------------------------
+# attention over the paged cache
+# ---------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class AttentionInputs:
+    q: np.ndarray              # uint16 [T, Hq, D] bf16 bits
+    row_offsets: np.ndarray    # uint32 [B + 1]
+    blocks: np.ndarray         # [L, 2, P, S, Hkv, D]: uint16 bf16 bits, or uint8 e4m3 codes
+    cache_lengths: np.ndarray  # uint32 [B]
+    page_table: np.ndarray     # uint32 [B, max_pages]
+    layer_idx: int
+    scales: np.ndarray | None = None   # e4m3 cache: float32 [L, 2, P, S, Hkv, D / gran]
+    gran: int = 0
+
+
+def attention_inputs(seed: int, new, history, hq: int, hkv: int, d: int, page: int = 16, gran: int = 0,
+                     layers: int = 2, spare_pages: int = 3, spare_rows: int = 0) -> AttentionInputs:
+    """New tokens and history per sequence; values N(0, 1) (e4m3: codes of N(0, 1) * 100 with
+    scales U(0.5, 2) / 100). Every slot that no sequence holds is NaN (e4m3: the NaN code and
+    a NaN scale) and every page table entry that no sequence needs is 0xFFFFFFFF. spare_rows:
+    rows of q behind the last sequence."""
+    rng = np.random.default_rng(seed)
+    new, history = np.asarray(new, dtype=np.int64), np.asarray(history, dtype=np.int64)
+    offs = np.concatenate([[0], np.cumsum(new)]).astype(np.uint32)
+    need = (new + history + page - 1) // page
+    pages = int(need.sum()) + spare_pages
+    perm = rng.permutation(pages)
+    table = np.full((len(new), int(need.max()) + 2), 0xFFFFFFFF, dtype=np.uint32)
+    at = 0
+    shape = (layers, 2, pages, page, hkv, d)
+    held = np.zeros((pages, page), bool)
+    for b in range(len(new)):
+        table[b, :need[b]] = perm[at:at + need[b]]
+        at += need[b]
+        pos = np.arange(new[b] + history[b])
+        held[table[b, pos // page], pos % page] = True
+    layer = layers - 1
+    values = rng.standard_normal(shape[1:])
+    if gran:
+        blocks = np.full(shape, 0x7F, dtype=np.uint8)
+        scales = np.full(shape[:5] + (d // gran,), np.nan, dtype=np.float32)
+        sc = (rng.uniform(0.5, 2.0, size=scales.shape[1:]) / 100).astype(np.float32)
+        blocks[layer][:, held] = e4m3_codes(values * 100)[:, held]
+        scales[layer][:, held] = sc[:, held]
+    else:
+        blocks = np.full(shape, 0xFFFF, dtype=np.uint16)
+        scales = None
+        blocks[layer][:, held] = bf16_bits(values)[:, held]
+    q = bf16_bits(rng.standard_normal((int(offs[-1]) + spare_rows, hq, d)))
+    return AttentionInputs(q=q, row_offsets=offs, blocks=blocks, cache_lengths=history.astype(np.uint32),
+                           page_table=table, layer_idx=layer, scales=scales, gran=gran)
