@@ -1,0 +1,208 @@
+// Shared by the attention kernels over the paged cache: how a call's work is cut
+// into items, e4m3 conversion, addresses of cache rows.
+//
+// A tile is BM consecutive (token, query head) rows of one sequence and one
+// key/value head. Its positions are cut into chunks, one work item each; tiles
+// of more than one chunk leave partial results in the workspace, which a second
+// kernel joins. Only the device knows the lengths, so every workgroup derives
+// the cut from them: with W the sum over the tiles of the positions they cover,
+//
+//   chunk = max(min_chunk, W / target) rounded up to the kernel's step
+//
+// which gives about target + tiles items of nearly equal size, whatever the mix
+// of lengths. A tile that is cut has fewer than 2 * positions / chunk items, so
+// all of them together have fewer than 2 * target: the workspace does not depend
+// on the batch or the lengths.
+#pragma once
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace qg {
+
+typedef int i32x2v_t __attribute__((ext_vector_type(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kAttnAlign = 32;   // a tile's first position is rounded down to this
+
+// What one workgroup works on.
+struct AttnItem {
+  int b;            // sequence, -1 past the last item
+  int tile;         // tile of the sequence's rows
+  int split;        // chunk of the tile's positions
+  int slots;        // workspace slot of (b, tile 0, head 0, split 0)
+  int nsplit;       // chunks reserved per tile of this sequence
+  int chunk;        // positions per chunk
+};
+
+// Tiles of a sequence, and the positions its longest tile may cover.
+__device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh, int bm) {
+  return (fresh * p.group + bm - 1) / bm;
+}
+__device__ __forceinline__ int attn_span(const AttnArgs& p, int len, int bm) {
+  if (!p.window) return len;
+  // a tile of bm rows has tokens t .. t + (bm - 1) / group + 1 at most
+  const long long w = (long long)p.window + (bm - 1) / p.group + 1 + kAttnAlign;
+  return (int)(w < len ? w : (long long)len);
+}
+
+template <int NT>
+struct AttnScan {
+  unsigned long long cost[NT / 64];
+  int items[NT / 64], slots[NT / 64];
+  AttnItem found;
+};
+
+// Item `want` of the launch (COUNT_SPLIT: among the tiles that are cut, one item
+// per tile; `split` is then 0). All NT threads call it. Items are ordered by
+// sequence, then chunk, then tile.
+template <int NT, bool COUNT_SPLIT>
+__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  unsigned long long cost = 0;
+  int fresh0 = 0, len0 = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += NT) {
+    const int b = b0 + tid;
+    if (b < p.batch) {
+      const int fresh = (int)(p.offs[b + 1] - p.offs[b]);
+      const int len = fresh + (int)p.cache_len[b];
+      if (b0 == 0) { fresh0 = fresh; len0 = len; }
+      cost += (unsigned long long)attn_tiles(p, fresh, p.bm) * (unsigned)attn_span(p, len, p.bm);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) cost += __shfl_xor(cost, d);
+  if (lane == 0) sh.cost[wave] = cost;
+  if (tid == 0) sh.found.b = -1;
+  __syncthreads();
+  cost = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) cost += sh.cost[w];
+  const unsigned long long even = (cost * (unsigned)p.hkv + p.target - 1) / (unsigned)p.target;
+  int chunk = even < (unsigned long long)p.min_chunk ? p.min_chunk : even > INT32_MAX / 2 ? INT32_MAX / 2 : (int)even;
+  chunk = (chunk + p.step - 1) / p.step * p.step;
+
+  int base = 0, slot_base = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += NT) {
+    const int b = b0 + tid;
+    int tiles = 0, ns = 0;
+    if (b < p.batch) {
+      const int fresh = b0 == 0 ? fresh0 : (int)(p.offs[b + 1] - p.offs[b]);
+      const int len = b0 == 0 ? len0 : fresh + (int)p.cache_len[b];
+      tiles = attn_tiles(p, fresh, p.bm);
+      if (tiles) ns = (attn_span(p, len, p.bm) + chunk - 1) / chunk;
+    }
+    const int items = COUNT_SPLIT ? (ns > 1 ? tiles : 0) : tiles * ns;
+    const int slots = ns > 1 ? tiles * ns * p.hkv : 0;
+    int ii = items, is = slots;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int vi = __shfl_up(ii, d), vs = __shfl_up(is, d);
+      if (lane >= d) { ii += vi; is += vs; }
+    }
+    if (lane == 63) { sh.items[wave] = ii; sh.slots[wave] = is; }
+    __syncthreads();
+    int bi = base, bs = slot_base;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+      if (w < wave) { bi += sh.items[w]; bs += sh.slots[w]; }
+      base += sh.items[w];
+      slot_base += sh.slots[w];
+    }
+    const int first = bi + ii - items;
+    if (want >= first && want < bi + ii) {
+      const int local = want - first;
+      sh.found = AttnItem{b, local % tiles, local / tiles, bs + is - slots, ns, chunk};
+    }
+    __syncthreads();
+    if (want < base) break;
+  }
+  AttnItem it = sh.found;
+  it.b = __builtin_amdgcn_readfirstlane(it.b);
+  it.tile = __builtin_amdgcn_readfirstlane(it.tile);
+  it.split = __builtin_amdgcn_readfirstlane(it.split);
+  it.slots = __builtin_amdgcn_readfirstlane(it.slots);
+  it.nsplit = __builtin_amdgcn_readfirstlane(it.nsplit);
+  it.chunk = __builtin_amdgcn_readfirstlane(it.chunk);
+  return it;
+}
+
+// The rows and positions of a tile.
+struct AttnTile {
+  int row0;               // the sequence's first row of q
+  int fresh, cached;
+  int r_first, r_count;   // rows of the sequence (token-major)
+  int t_first, t_last;    // their tokens
+  int begin, end;         // positions that some row sees: [begin, end)
+  int start;              // begin rounded down
+};
+
+__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, int b, int tile) {
+  AttnTile t;
+  t.row0 = (int)p.offs[b];
+  t.fresh = (int)p.offs[b + 1] - t.row0;
+  t.cached = (int)p.cache_len[b];
+  t.r_first = tile * p.bm;
+  t.r_count = min(t.fresh * p.group - t.r_first, p.bm);
+  t.t_first = t.r_first / p.group;
+  t.t_last = (t.r_first + t.r_count - 1) / p.group;
+  t.end = p.causal ? t.cached + t.t_last + 1 : t.cached + t.fresh;
+  t.begin = p.window ? max(0, t.cached + t.t_first - p.window + 1) : 0;
+  t.start = t.begin / kAttnAlign * kAttnAlign;
+  return t;
+}
+
+// x / d for the divisor that (mul, shift) were made for; x < 2^31
+__device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t mul, uint32_t shift) {
+  return (__umulhi(x, mul) + x) >> shift;
+}
+
+// four e4m3 codes -> four bf16 (exact)
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false));
+  hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true));
+}
+
+// global_load_lds with a 64-bit address per lane: lane l's 16 (4) bytes land at
+// LDS byte lds + 16 l (4 l), for the lanes that are active. The issuer counts its
+// loads and waits for them with wait_loads.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void dma16_at(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(at) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_at(const void* at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(at) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// until at most N of this wave's vector-memory loads are in flight
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// until this wave's LDS reads have returned (before a load into the same place)
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// eight transposed bf16 rows x 16 columns: see the kernels for the lanes' order
+__device__ __forceinline__ uint64_t lds_read_tr16(const void* p) {
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                          (__attribute__((address_space(3))) s16x4_t*)(const_cast<void*>(p))));
+}
+__device__ __forceinline__ uint64_t lds_read_tr8(const void* p) {
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                                          (__attribute__((address_space(3))) i32x2v_t*)(const_cast<void*>(p))));
+}
+
+// Floats of a workspace slot: the rows' outputs, then their maxima and sums.
+__host__ __device__ constexpr long long attn_slot_floats(int bm, int dp) { return (long long)bm * (dp + 2); }
+
+hipError_t launch_attention_rows(AttnArgs p, int mt, hipStream_t stream);
+hipError_t launch_attention_tiles(AttnArgs p, hipStream_t stream);
+
+}  // namespace qg

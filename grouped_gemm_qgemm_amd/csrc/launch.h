@@ -119,6 +119,9 @@ struct AttnArgs {
   int64_t T, max_pages, pages;
   int batch, hq, hkv, group, d, page_size, layer, gran, causal, window, fp8, num_cus;
   float scale;
+  // the launcher's: page_size as a multiplication, and how the work is cut (attention_common.h)
+  uint32_t div_mul = 0, div_shift = 0;
+  int bm = 0, target = 0, min_chunk = 0, step = 0;
 };
 
 // Decode-shaped W4A16 (M <= 16).
