@@ -17,6 +17,7 @@ namespace {
 
 constexpr int JT = 256;
 constexpr int kRowsTarget = 1024, kRowsMinChunk = 512, kRowsStep = 128;
+constexpr int kTileTarget = 1024, kTileMinChunk = 512, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
@@ -113,8 +114,9 @@ static hipError_t launch_join(const AttnArgs& p, int rows_per_wg, hipStream_t st
 
 int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t hkv, int64_t d) {
   (void)T; (void)batch; (void)hq;
-  const int64_t target = kRowsTarget > hkv ? kRowsTarget : hkv;
-  return 2 * target * attn_slot_floats(32, dp_of(d));
+  const int64_t rows_target = kRowsTarget > hkv ? kRowsTarget : hkv, tile_target = kTileTarget > hkv ? kTileTarget : hkv;
+  const int64_t rows = 2 * rows_target * attn_slot_floats(32, dp_of(d)), tile = 2 * tile_target * attn_slot_floats(128, dp_of(d));
+  return rows > tile ? rows : tile;
 }
 
 hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
@@ -125,15 +127,16 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   p.div_shift = shift;
   p.div_mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)p.page_size)) / (uint64_t)p.page_size) + 1);
   const long long rows = p.T * p.group;
-  if (rows > 32LL * p.batch) return launch_attention_tiles(p, stream);
+  const bool few = rows <= 32LL * p.batch;
   const int mt = rows > 16LL * p.batch ? 2 : 1;
-  p.bm = 16 * mt;
-  p.target = kRowsTarget > p.hkv ? kRowsTarget : p.hkv;
-  p.min_chunk = kRowsMinChunk;
-  p.step = kRowsStep;
-  hipError_t e = launch_attention_rows(p, mt, stream);
+  p.bm = few ? 16 * mt : 128;
+  p.target = few ? kRowsTarget : kTileTarget;
+  if (p.target < p.hkv) p.target = p.hkv;
+  p.min_chunk = few ? kRowsMinChunk : kTileMinChunk;
+  p.step = few ? kRowsStep : kTileStep;
+  const hipError_t e = few ? launch_attention_rows(p, mt, stream) : launch_attention_tiles(p, stream);
   if (e != hipSuccess || p.max_pages * p.page_size <= p.min_chunk) return e;   // nothing can be cut
-  return launch_join(p, 1, stream);
+  return launch_join(p, few ? 1 : 16, stream);
 }
 
 }  // namespace qg

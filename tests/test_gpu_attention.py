@@ -74,7 +74,7 @@ def compare(d, got, ref, what=""):
     fine = np.isfinite(o)
     assert np.array_equal(g[~fine & ~np.isnan(o)], o[~fine & ~np.isnan(o)]), what
     tol = tolerance(d, ref)[:rows]
-    err = np.abs(g - o)
+    err = np.abs(np.where(fine, g, 0) - np.where(fine, o, 0))
     over = fine & (err > tol)
     if over.any():
         i = tuple(np.argwhere(over)[0])
@@ -92,21 +92,25 @@ def check(lib, d, scale=None, causal=True, window=0, what=""):
     return got
 
 
+# few rows per sequence, and many: one kernel for each
 RAGGED = ([3, 0, 1, 7, 2], [0, 5, 40, 61, 130])
+CHUNKS = ([70, 0, 33, 1, 129], [0, 5, 40, 61, 130])
 
 
 @pytest.mark.parametrize("gran,dim", [(0, 8), (0, 64), (0, 72), (0, 96), (0, 128), (0, 136), (0, 256), (32, 32), (32, 64),
                                       (64, 64), (32, 96), (32, 128), (64, 128), (128, 128), (64, 192), (32, 256), (64, 256),
                                       (128, 256)])
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2)])
-def test_head_dims_and_scale_runs(lib, gpu, gran, dim, hq, hkv):
-    check(lib, synth.attention_inputs(11, *RAGGED, hq=hq, hkv=hkv, d=dim, gran=gran, spare_rows=3))
+@pytest.mark.parametrize("lengths", [RAGGED, CHUNKS], ids=["few", "chunks"])
+def test_head_dims_and_scale_runs(lib, gpu, gran, dim, hq, hkv, lengths):
+    check(lib, synth.attention_inputs(11, *lengths, hq=hq, hkv=hkv, d=dim, gran=gran, spare_rows=3))
 
 
 @pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 8), (7, 1), (6, 2), (10, 2), (16, 1), (17, 1), (32, 2), (40, 1), (130, 1)])
 @pytest.mark.parametrize("gran", [0, 64])
-def test_head_groups(lib, gpu, hq, hkv, gran):
-    check(lib, synth.attention_inputs(12, *RAGGED, hq=hq, hkv=hkv, d=64, gran=gran))
+@pytest.mark.parametrize("lengths", [RAGGED, CHUNKS], ids=["few", "chunks"])
+def test_head_groups(lib, gpu, hq, hkv, gran, lengths):
+    check(lib, synth.attention_inputs(12, *lengths, hq=hq, hkv=hkv, d=64, gran=gran))
 
 
 @pytest.mark.parametrize("page", [1, 3, 16, 48, 128])
@@ -144,12 +148,32 @@ def test_not_causal(lib, gpu, gran):
 def test_long_history_is_split(lib, gpu, gran):
     check(lib, synth.attention_inputs(18, [1, 2, 1], [9000, 40, 2500], hq=4, hkv=1, d=128, page=64, gran=gran, layers=1))
     check(lib, synth.attention_inputs(19, [40], [5000], hq=4, hkv=1, d=128, page=64, gran=gran, layers=1))
+    check(lib, synth.attention_inputs(19, [2, 90, 0, 1], [2000, 5000, 3, 40], hq=4, hkv=1, d=64, page=1, gran=gran and 64,
+                                      layers=1))
+    check(lib, synth.attention_inputs(19, [3, 2, 0, 1], [2000, 5000, 3, 40], hq=4, hkv=1, d=64, page=1, gran=gran and 64,
+                                      layers=1), window=1500)
 
 
 @pytest.mark.parametrize("scale", [1e-6, 1.0, 30.0])
-def test_scales(lib, gpu, scale):
+@pytest.mark.parametrize("new", [[5, 3], [5, 150]], ids=["few", "chunks"])
+def test_scales(lib, gpu, scale, new):
     """From nearly even weights to a single one."""
-    check(lib, synth.attention_inputs(20, [5, 50], [90, 20], hq=4, hkv=2, d=64), scale=scale)
+    check(lib, synth.attention_inputs(20, new, [90, 20], hq=4, hkv=2, d=64), scale=scale)
+
+
+@pytest.mark.parametrize("new", [[2], [100]], ids=["few", "chunks"])
+@pytest.mark.parametrize("order", [1, -1])
+def test_scores_that_grow_along_the_sequence(lib, gpu, new, order):
+    """The running maximum moves at every block (or never after the first)."""
+    d = synth.attention_inputs(34, new, [900], hq=4, hkv=2, d=64)
+    n = 900 + new[0]
+    page, slot = d.page_table[0, np.arange(n) // 16], np.arange(n) % 16
+    size = np.linspace(0.0, 40.0, n)[::order]
+    k = np.zeros((n, 2, 64))
+    k[:, :, 0] = size[:, None]
+    d.blocks[1, 0, page, slot] = synth.bf16_bits(k)
+    d.q[:] = synth.bf16_bits(np.broadcast_to(np.eye(64)[0], d.q.shape))
+    check(lib, d, scale=1.0)
 
 
 def test_constant_values_come_back(lib, gpu):
@@ -173,12 +197,13 @@ def test_page_table_entries_of_an_evicted_prefix_are_not_read(lib, gpu):
 @pytest.mark.parametrize("plane", [0, 1])
 @pytest.mark.parametrize("bad", ["nan", "inf", "-inf"])
 @pytest.mark.parametrize("window", [0, 9])
-def test_what_a_row_must_not_see_does_not_reach_it(lib, gpu, gran, plane, bad, window):
+@pytest.mark.parametrize("new", [[40, 2, 1], [150, 2, 1]], ids=["few", "chunks"])
+def test_what_a_row_must_not_see_does_not_reach_it(lib, gpu, gran, plane, bad, window, new):
     """One position of a chunk holds infinities or NaN: the tokens before it (and, with a
     window, far behind it) are as without it, and those that see it are as the formula says."""
     if gran and bad != "nan" and plane == 0:
         pytest.skip("e4m3 has no infinities; an infinite key scale is the NaN case of the scores")
-    d = synth.attention_inputs(23, [40, 2, 1], [70, 3, 60], hq=4, hkv=2, d=64, page=16, gran=gran)
+    d = synth.attention_inputs(23, new, [70, 3, 60], hq=4, hkv=2, d=64, page=16, gran=gran)
     at = 70 + 17
     page, slot = d.page_table[0, at // 16], at % 16
     value = float(bad)
@@ -194,9 +219,9 @@ def test_what_a_row_must_not_see_does_not_reach_it(lib, gpu, gran, plane, bad, w
         # a score of +infinity has no softmax; one of -infinity is a weight of zero
         rows = np.isfinite(ref[0]).all(axis=(1, 2))
         sees = np.zeros(len(d.q), bool)
-        sees[17:40] = True
+        sees[17:new[0]] = True
         if window:
-            sees[17 + window:40] = False
+            sees[17 + window:new[0]] = False
         assert rows[~sees].all()
         g = bf16v(got)
         assert (np.abs(g - ref[0]) <= tolerance(d, ref))[~sees].all()
@@ -206,8 +231,9 @@ def test_what_a_row_must_not_see_does_not_reach_it(lib, gpu, gran, plane, bad, w
     assert np.isfinite(before).all()
 
 
-def test_a_bad_query_reaches_its_own_row_only(lib, gpu):
-    d = synth.attention_inputs(24, [6, 3], [40, 9], hq=4, hkv=2, d=64)
+@pytest.mark.parametrize("new", [[6, 3], [160, 3]], ids=["few", "chunks"])
+def test_a_bad_query_reaches_its_own_row_only(lib, gpu, new):
+    d = synth.attention_inputs(24, new, [40, 9], hq=4, hkv=2, d=64)
     d.q[2, 1, 3] = 0x7FC0
     got, ref = run(lib, d, 0.125), exact(d, 0.125)
     g = bf16v(got)
