@@ -34,6 +34,7 @@ struct AttnItem {
   int slots;        // workspace slot of (b, tile 0, head 0, split 0)
   int nsplit;       // chunks reserved per tile of this sequence
   int chunk;        // positions per chunk
+  int row0, fresh, cached;   // the sequence's first row of q, new tokens, history
 };
 
 // Tiles of a sequence, and the positions its longest tile may cover.
@@ -61,13 +62,13 @@ template <int NT, bool COUNT_SPLIT>
 __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   unsigned long long cost = 0;
-  int fresh0 = 0, len0 = 0;
+  int row00 = 0, fresh0 = 0, len0 = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
     if (b < p.batch) {
-      const int fresh = (int)(p.offs[b + 1] - p.offs[b]);
+      const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
-      if (b0 == 0) { fresh0 = fresh; len0 = len; }
+      if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
       cost += (unsigned long long)attn_tiles(p, fresh, p.bm) * (unsigned)attn_span(p, len, p.bm);
     }
   }
@@ -86,10 +87,13 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
   int base = 0, slot_base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
-    int tiles = 0, ns = 0;
+    int tiles = 0, ns = 0, row0 = row00, fresh = fresh0, len = len0;
     if (b < p.batch) {
-      const int fresh = b0 == 0 ? fresh0 : (int)(p.offs[b + 1] - p.offs[b]);
-      const int len = b0 == 0 ? len0 : fresh + (int)p.cache_len[b];
+      if (b0 > 0) {
+        row0 = (int)p.offs[b];
+        fresh = (int)p.offs[b + 1] - row0;
+        len = fresh + (int)p.cache_len[b];
+      }
       tiles = attn_tiles(p, fresh, p.bm);
       if (tiles) ns = (attn_span(p, len, p.bm) + chunk - 1) / chunk;
     }
@@ -113,7 +117,8 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
     const int first = bi + ii - items;
     if (want >= first && want < bi + ii) {
       const int local = want - first;
-      sh.found = AttnItem{b, local % tiles, local / tiles, bs + is - slots, ns, chunk};
+      // the last tiles, which see the most positions, first
+      sh.found = AttnItem{b, tiles - 1 - local % tiles, local / tiles, bs + is - slots, ns, chunk, row0, fresh, len - fresh};
     }
     __syncthreads();
     if (want < base) break;
@@ -125,30 +130,28 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
   it.slots = __builtin_amdgcn_readfirstlane(it.slots);
   it.nsplit = __builtin_amdgcn_readfirstlane(it.nsplit);
   it.chunk = __builtin_amdgcn_readfirstlane(it.chunk);
+  it.row0 = __builtin_amdgcn_readfirstlane(it.row0);
+  it.fresh = __builtin_amdgcn_readfirstlane(it.fresh);
+  it.cached = __builtin_amdgcn_readfirstlane(it.cached);
   return it;
 }
 
 // The rows and positions of a tile.
 struct AttnTile {
-  int row0;               // the sequence's first row of q
-  int fresh, cached;
   int r_first, r_count;   // rows of the sequence (token-major)
   int t_first, t_last;    // their tokens
   int begin, end;         // positions that some row sees: [begin, end)
   int start;              // begin rounded down
 };
 
-__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, int b, int tile) {
+__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem& it) {
   AttnTile t;
-  t.row0 = (int)p.offs[b];
-  t.fresh = (int)p.offs[b + 1] - t.row0;
-  t.cached = (int)p.cache_len[b];
-  t.r_first = tile * p.bm;
-  t.r_count = min(t.fresh * p.group - t.r_first, p.bm);
+  t.r_first = it.tile * p.bm;
+  t.r_count = min(it.fresh * p.group - t.r_first, p.bm);
   t.t_first = t.r_first / p.group;
   t.t_last = (t.r_first + t.r_count - 1) / p.group;
-  t.end = p.causal ? t.cached + t.t_last + 1 : t.cached + t.fresh;
-  t.begin = p.window ? max(0, t.cached + t.t_first - p.window + 1) : 0;
+  t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
+  t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
   t.start = t.begin / kAttnAlign * kAttnAlign;
   return t;
 }
@@ -177,6 +180,11 @@ __device__ __forceinline__ void dma4_at(const void* at, uint32_t lds) {
 }
 #pragma clang diagnostic pop
 
+// Makes the compiler wait here for what it loads into x itself. Its waits count
+// only the loads it knows of: left to the first use inside a loop, one would wait
+// for the loop's direct-to-LDS loads as well, in every iteration.
+__device__ __forceinline__ void arrived(u32x4_t& x) { asm volatile("" : "+v"(x)); }
+
 // until at most N of this wave's vector-memory loads are in flight
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -187,6 +195,19 @@ __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// the larger of x and the other half-wave's x
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  const uint32_t a = r[0], b = r[1];
+  return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+// the larger of x in lanes l and l ^ 16
+__device__ __forceinline__ float max_quarters(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+  const uint32_t a = r[0], b = r[1];
+  return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
 // eight transposed bf16 rows x 16 columns: see the kernels for the lanes' order

@@ -17,7 +17,7 @@ namespace {
 
 constexpr int JT = 256;
 constexpr int kRowsTarget = 1024, kRowsMinChunk = 512, kRowsStep = 128;
-constexpr int kTileTarget = 1024, kTileMinChunk = 512, kTileStep = 64;
+constexpr int kTileTarget = 512, kTileMinChunk = 512, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
@@ -35,7 +35,7 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int rows
   const int h = blockIdx.x % p.hkv, at = blockIdx.x / p.hkv;
   const AttnItem it = attn_locate<JT, true>(p, at / parts, scan);
   if (it.b < 0) return;
-  const AttnTile t = attn_tile(p, it.b, it.tile);
+  const AttnTile t = attn_tile(p, it);
   const int ns = (t.end - t.start + it.chunk - 1) / it.chunk;
   if (ns <= 1) return;   // written by its only chunk
   const long long slot_floats = attn_slot_floats(p.bm, DP);
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int rows
     }
     const float inv = 1.f / sum;
     const int row = t.r_first + r;
-    uint16_t* to = p.out + ((size_t)(t.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
+    uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
 #pragma unroll
     for (int i = 0; i < VL; ++i)
       if (lane * VL + i < p.d) to[lane * VL + i] = (uint16_t)f2bf2_rn(o[i] * inv, 0.f);

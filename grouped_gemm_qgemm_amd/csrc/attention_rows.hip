@@ -60,29 +60,33 @@ __global__ __launch_bounds__(NW * 64) void attention_rows_kernel(AttnArgs p) {
   const int h = blockIdx.x % p.hkv;
   const AttnItem it = attn_locate<NT, false>(p, blockIdx.x / p.hkv, scan);
   if (it.b < 0) return;
-  const AttnTile t = attn_tile(p, it.b, it.tile);
+  const AttnTile t = attn_tile(p, it);
   const int c_first = t.start + it.split * it.chunk;          // this item's positions [c_first, c_end)
   const int c_end = min(t.end, c_first + it.chunk);
   if (c_first >= c_end) return;                               // the sequence's longer tiles need this chunk
   const bool alone = t.end - t.start <= it.chunk;
 
   // rows of this lane, one per 16-row tile
-  const int rows = t.fresh * p.group;
+  const int rows = it.fresh * p.group;
   int tok[MT], hi[MT], lo[MT];
   u32x4_t qf[MT][NS];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = min(t.r_first + 16 * mt + col, rows - 1);
     tok[mt] = r / p.group;
-    hi[mt] = p.causal ? t.cached + tok[mt] : t.cached + t.fresh - 1;
-    lo[mt] = p.window ? t.cached + tok[mt] - p.window + 1 : 0;
-    const uint16_t* q = p.q + ((size_t)(t.row0 + tok[mt]) * p.hq + h * p.group + r % p.group) * p.d;
+    hi[mt] = p.causal ? it.cached + tok[mt] : it.cached + it.fresh - 1;
+    lo[mt] = p.window ? it.cached + tok[mt] - p.window + 1 : 0;
+    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[mt]) * p.hq + h * p.group + r % p.group) * p.d;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int d = 32 * s + 8 * j;
       qf[mt][s] = d < p.d ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
     }
   }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) arrived(qf[mt][s]);
   const int runs = FP8 ? p.d / p.gran : 1;
   const int run_steps = FP8 ? p.gran / 32 : NS;
   const int chunks = p.d * ES / 16;                           // chunks of a cache row that exist
@@ -199,23 +203,22 @@ __global__ __launch_bounds__(NW * 64) void attention_rows_kernel(AttnArgs p) {
             for (int mt = 0; mt < MT; ++mt) sc[mt][nb] = part[mt];
           }
         }
-        const bool masked = (p.window && k0 < t.cached + t.t_last - p.window + 1) || k0 < t.begin ||
-                            k0 + 32 > min(s_end, p.causal ? t.cached + t.t_first + 1 : t.end);
+        const bool masked = (p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
+                            k0 + 32 > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end);
         u32x4_t pf[MT][2];    // probabilities: value and remainder
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           if (masked) {
+            // positions lo .. min(hi, s_end - 1), counted from lo
+            const uint32_t seen = max(min(hi[mt], s_end - 1) - lo[mt] + 1, 0), first = k0 + 4 * j - lo[mt];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int pos = k0 + 16 * (e >> 2) + 4 * j + (e & 3);
-              if (pos > hi[mt] || pos < lo[mt] || pos >= s_end) sc[mt][e >> 2][e & 3] = -INFINITY;
-            }
+            for (int e = 0; e < 8; ++e)
+              sc[mt][e >> 2][e & 3] = first + (16 * (e >> 2) + (e & 3)) < seen ? sc[mt][e >> 2][e & 3] : -INFINITY;
           }
           float mx = m[mt];
 #pragma unroll
           for (int e = 0; e < 8; ++e) mx = fmaxf(mx, sc[mt][e >> 2][e & 3]);
-          mx = fmaxf(mx, __shfl_xor(mx, 16));
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
+          mx = max_halves(max_quarters(mx));
           // a row that has seen nothing yet keeps m = -infinity; its probabilities are 0
           const float base = mx == -INFINITY ? 0.f : mx * cs;
           const float alpha = __builtin_amdgcn_exp2f((m[mt] == -INFINITY ? -INFINITY : m[mt] * cs) - base);
@@ -292,8 +295,8 @@ __global__ __launch_bounds__(NW * 64) void attention_rows_kernel(AttnArgs p) {
             } else {
               // token by token, with the values it does not see set to zero
               for (int tt = t.t_first; tt <= t.t_last; ++tt) {
-                const int t_hi = p.causal ? t.cached + tt : t.cached + t.fresh - 1;
-                const int t_lo = p.window ? t.cached + tt - p.window + 1 : 0;
+                const int t_hi = p.causal ? it.cached + tt : it.cached + it.fresh - 1;
+                const int t_lo = p.window ? it.cached + tt - p.window + 1 : 0;
                 uint32_t keep[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -357,7 +360,7 @@ __global__ __launch_bounds__(NW * 64) void attention_rows_kernel(AttnArgs p) {
       if (d < p.d) {
         const int row = t.r_first + r;
         const float inv = 1.f / sum;   // every row sees a position
-        uint16_t* to = p.out + ((size_t)(t.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d + d;
+        uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d + d;
         *reinterpret_cast<u32x2_t*>(to) = u32x2_t{f2bf2_rn(o[0] * inv, o[1] * inv), f2bf2_rn(o[2] * inv, o[3] * inv)};
       }
     } else {

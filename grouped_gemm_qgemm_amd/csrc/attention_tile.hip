@@ -29,8 +29,6 @@
 // Its value row is still multiplied, by zero: where it holds an infinity or NaN
 // the row's output would turn NaN. So a tile whose result is not finite is
 // computed again with the values selected per token.
-#include <type_traits>
-
 #include "attention_common.h"
 
 namespace qg {
@@ -55,56 +53,68 @@ __device__ __forceinline__ int swz_tv(int r) {
 
 }  // namespace
 
-// GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16
-template <int DP, int GRAN, int RT>
-__global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) {
+// LDS of a workgroup.
+template <int DP, int GRAN>
+struct AttnTileLds {
+  static constexpr int KB = DP > 128 ? 32 : 64;             // positions per block
+  static constexpr int R = GRAN > 0 ? DP / GRAN : 1;        // scale runs per head, at most
+  __attribute__((aligned(16))) u32x4_t ring[2][2][KB * DP / 8];                                   // [block parity][keys, values]
+  __attribute__((aligned(16))) float ring_s[GRAN > 0 ? 2 : 1][2][R][GRAN > 0 ? KB : 1];   // [keys, values][run][position]
+  uint32_t pages[TPG];
+  AttnScan<AW * 64> scan;
+};
+
+// One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
+// values are selected per token. Without it, returns whether some output came out
+// as an infinity or NaN, for the whole workgroup, and then has written nothing.
+template <int DP, int GRAN, int RT, bool SAFE>
+__device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int NT = AW * 64;
-  constexpr int KB = DP > 128 ? 32 : 64;      // positions per block
+  constexpr int KB = AttnTileLds<DP, GRAN>::KB;
   constexpr int NB = KB / 32;
   constexpr int NS = DP / 16;                 // MFMA steps of a score
   constexpr int ND = DP / 32;                 // 32-wide strips of the output
   constexpr int CH = DP / 8;                  // 16-byte chunks per LDS row
   constexpr int TILE = KB * CH;
   constexpr int LD = TILE / NT;               // direct loads per lane for the keys (or values) of a block
-  constexpr int R = FP8 ? DP / GRAN : 1;      // scale runs per head, at most
+  constexpr int R = AttnTileLds<DP, GRAN>::R;
   constexpr int RS = FP8 ? GRAN / 16 : NS;    // MFMA steps per run
   constexpr int LC = FP8 ? DP / 16 : 1;       // e4m3: 16-code loads per row
   constexpr int LQ = FP8 ? KB * LC / NT : 0;  // e4m3: loads per thread for the keys (or values)
   constexpr int LS = FP8 ? (2 * KB * R + NT - 1) / NT : 0;   // scales per thread
-  __shared__ __attribute__((aligned(16))) u32x4_t ring[2][2][TILE];                 // [block parity][keys, values]
-  __shared__ __attribute__((aligned(16))) float ring_s[FP8 ? 2 : 1][2][R][FP8 ? KB : 1];   // [keys, values][run][position]
-  __shared__ uint32_t pages[TPG];
-  __shared__ AttnScan<NT> scan;
-
+  auto& ring = lds.ring;
+  auto& ring_s = lds.ring_s;
+  auto& pages = lds.pages;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const int h = blockIdx.x % p.hkv;
-  AttnItem it = attn_locate<NT, false>(p, blockIdx.x / p.hkv, scan);
-  if (it.b < 0) return;
-  const AttnTile t = attn_tile(p, it.b, it.tile);
+  const AttnTile t = attn_tile(p, it);
   const int c_first = t.start + it.split * it.chunk;          // this item's positions [c_first, c_end)
   const int c_end = min(t.end, c_first + it.chunk);
-  if (c_first >= c_end) return;                               // the sequence's longer tiles need this chunk
+  if (c_first >= c_end) return false;                               // the sequence's longer tiles need this chunk
   const bool alone = t.end - t.start <= it.chunk;
 
-  const int rows = t.fresh * p.group;
+  const int rows = it.fresh * p.group;
   int tok[RT], hi[RT], lo[RT];
   u32x4_t qf[RT][NS];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = min(t.r_first + (wave * RT + rt) * 32 + col, rows - 1);
     tok[rt] = r / p.group;
-    hi[rt] = p.causal ? t.cached + tok[rt] : t.cached + t.fresh - 1;
-    lo[rt] = p.window ? t.cached + tok[rt] - p.window + 1 : 0;
-    const uint16_t* q = p.q + ((size_t)(t.row0 + tok[rt]) * p.hq + h * p.group + r % p.group) * p.d;
+    hi[rt] = p.causal ? it.cached + tok[rt] : it.cached + it.fresh - 1;
+    lo[rt] = p.window ? it.cached + tok[rt] - p.window + 1 : 0;
+    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[rt]) * p.hq + h * p.group + r % p.group) * p.d;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int d = 16 * s + 8 * half;
       qf[rt][s] = d < p.d ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
     }
   }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) arrived(qf[rt][s]);
   const float cs = p.scale * kLog2e;
   const int runs = FP8 ? p.d / (FP8 ? GRAN : 1) : 1;
   const int chunks = p.d / 8;                                 // chunks of an LDS row that exist
@@ -120,9 +130,7 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
 
   float16_t acc[RT][ND];
   float m[RT], l[RT];     // reference of the weights' exponents (base 2), this lane's share of their sum
-  // SAFE: the pass that selects values per token
-  auto attend = [&](auto safe) {
-    constexpr bool SAFE = decltype(safe)::value;
+  {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       m[rt] = -INFINITY;
@@ -253,18 +261,19 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
             for (int rt = 0; rt < RT; ++rt) sc[rt][nb] = part[rt];
           }
         }
-        const bool masked = (p.window && k0 < t.cached + t.t_last - p.window + 1) || k0 < t.begin ||
-                            k0 + KB > min(s_end, p.causal ? t.cached + t.t_first + 1 : t.end);
+        const bool masked = (p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
+                            k0 + KB > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end);
         if (masked) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+          for (int rt = 0; rt < RT; ++rt) {
+            // positions lo .. min(hi, s_end - 1), counted from lo
+            const uint32_t seen = max(min(hi[rt], s_end - 1) - lo[rt] + 1, 0), first = k0 + 4 * half - lo[rt];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int pos = k0 + nb * 32 + 8 * (e / 4) + 4 * half + e % 4;
-                if (pos > hi[rt] || pos < lo[rt] || pos >= s_end) sc[rt][nb][e] = -INFINITY;
-              }
+              for (int e = 0; e < 16; ++e)
+                sc[rt][nb][e] = first + (nb * 32 + 8 * (e / 4) + e % 4) < seen ? sc[rt][nb][e] : -INFINITY;
+          }
         }
         float base[RT];
 #pragma unroll
@@ -274,7 +283,7 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[rt][nb][e]);
-          mx = fmaxf(mx, __shfl_xor(mx, 32)) * cs;
+          mx = max_halves(mx) * cs;
           if (__any(mx > m[rt] + kSlack || (m[rt] == -INFINITY && mx > -INFINITY))) {
             const float top = fmaxf(m[rt], mx);
             const float alpha = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[rt] - top);
@@ -362,8 +371,8 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
                   const u32x4_t pf = weights(rt, nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
 #pragma unroll 1
                   for (int tt = t.t_first; tt <= t.t_last; ++tt) {
-                    const int t_hi = p.causal ? t.cached + tt : t.cached + t.fresh - 1;
-                    const int t_lo = p.window ? t.cached + tt - p.window + 1 : 0;
+                    const int t_hi = p.causal ? it.cached + tt : it.cached + it.fresh - 1;
+                    const int t_lo = p.window ? it.cached + tt - p.window + 1 : 0;
                     uint32_t keep[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -391,9 +400,8 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
       for (int n = 0; n < ND; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[rt][n][e]) < INFINITY);
-    return off;
-  };
-  if (__syncthreads_or(attend(std::false_type{}))) attend(std::true_type{});
+    if (!SAFE && __syncthreads_or(off)) return true;
+  }
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
   float* ws = p.workspace + (size_t)slot * attn_slot_floats(p.bm, DP);
@@ -405,7 +413,7 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
     if (alone) {
       const float inv = 1.f / sum;   // every row sees a position
       const int row = t.r_first + r;
-      uint16_t* to = p.out + ((size_t)(t.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
+      uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
 #pragma unroll
       for (int n = 0; n < ND; ++n)
 #pragma unroll
@@ -428,6 +436,25 @@ __global__ __launch_bounds__(AW * 64, 2) void attention_tile_kernel(AttnArgs p) 
       }
     }
   }
+  return false;
+}
+
+// Called, not inlined: hardly ever taken, and its registers stay out of the
+// kernel's. The arguments are read again where the kernel got them, since a copy
+// of them to pass would be written to memory by every lane.
+template <int DP, int GRAN, int RT>
+__device__ __attribute__((noinline)) void attend_tile_safe(const AttnArgs* p, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
+  attend_tile<DP, GRAN, RT, true>(*p, it, blockIdx.x % p->hkv, *lds);
+}
+
+template <int DP, int GRAN, int RT>
+__global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
+  __shared__ AttnTileLds<DP, GRAN> lds;
+  const int h = blockIdx.x % p.hkv;
+  const AttnItem it = attn_locate<AW * 64, false>(p, blockIdx.x / p.hkv, lds.scan);
+  if (it.b < 0) return;
+  if (attend_tile<DP, GRAN, RT, false>(p, it, h, lds))
+    attend_tile_safe<DP, GRAN, RT>((const AttnArgs*)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
 }
 
 hipError_t launch_attention_tiles(AttnArgs p, hipStream_t stream) {
