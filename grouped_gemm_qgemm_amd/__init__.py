@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -119,10 +120,11 @@ def load(path: str | None = None):
     lib.k_matmul_ragged_paged_scale.restype = ctypes.c_int
     lib.kv_matmul_ragged_paged_scale.argtypes = lib.k_matmul_ragged_paged_scale.argtypes
     lib.kv_matmul_ragged_paged_scale.restype = ctypes.c_int
-    lib.tables_ragged_paged.argtypes = [T, T, T, T, T, T, T, T, ctypes.c_int32, ctypes.c_void_p]
+    V = ctypes.c_void_p   # a descriptor by address: byref(QgTensor), or its bytes (see _record)
+    lib.tables_ragged_paged.argtypes = [V, V, V, V, V, V, V, V, ctypes.c_int32, V]
     lib.tables_ragged_paged.restype = ctypes.c_int
-    lib.attention_ragged_paged.argtypes = [T, T, T, ctypes.POINTER(QgPagedKV), ctypes.c_uint32, ctypes.c_float,
-                                           ctypes.c_int32, ctypes.c_int32, T, ctypes.c_void_p]
+    lib.attention_ragged_paged.argtypes = [V, V, V, V, ctypes.c_uint32, ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
+                                           V, V]
     lib.attention_ragged_paged.restype = ctypes.c_int
     lib.attention_ragged_paged_workspace.argtypes = [ctypes.c_int64] * 5
     lib.attention_ragged_paged_workspace.restype = ctypes.c_int64
@@ -344,28 +346,58 @@ def kv_matmul_ragged_paged_scale(hidden, input_row_offsets, weight, input_scale,
                     kv_scales, quantization_granularity, stream, raise_on_error)
 
 
-def _device_of(tensors):
-    """The GPU that all of a call's tensors are on."""
+# The calls of a decode step take a few microseconds on the GPU, so describing their
+# tensors has to cost less: a qg_tensor as the bytes of its fields, by rank
+# (0.4 us where filling a ctypes structure takes 0.8 us).
+_RECORD = [struct.Struct(f"<Qii{n}q{8 * (MAX_RANK - n)}x").pack for n in range(MAX_RANK + 1)]
+_KV_TABLES = struct.Struct("<QQq").pack
+_KV_GRANULARITY = struct.Struct("<q").pack
+_NO_TENSOR = _RECORD[0](0, 0, 0)
+_TABLE_DTYPE = {torch.int32: QG.U32, torch.uint32: QG.U32}     # tables of uint32 may be held in int32
+_CACHE_DTYPE = {**_TORCH_TO_QG, torch.uint8: QG.FP8_E4M3}      # e4m3 codes may be held in uint8
+
+
+def _record(t, dtypes=_TORCH_TO_QG):
+    """The bytes of describe(t); None (a NULL descriptor) for None."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to the library must be contiguous")
+    shape = t.shape
+    if len(shape) > MAX_RANK:
+        raise ValueError("rank above 6")
+    return _RECORD[len(shape)](t.data_ptr(), dtypes.get(t.dtype, -1), len(shape), *shape)
+
+
+def _device_of(tensors) -> int:
+    """Index of the GPU that all of a call's tensors are on."""
     dev = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("tensors passed to the library must be on a GPU")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("tensors of one call must be on one GPU")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if d < 0:
+                    raise ValueError("tensors passed to the library must be on a GPU")
+                if dev is not None:
+                    raise ValueError("tensors of one call must be on one GPU")
+                dev = d
     return dev
 
 
-def _on(dev, stream, call):
-    """call(stream) with the tensors' GPU as the current one; the default stream is
+# the current stream's handle without building a torch.cuda.Stream (2.7 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _launch(fn, dev, stream, *args) -> int:
+    """fn(*args, stream) with the tensors' GPU as the current one; the default stream is
     that GPU's current stream."""
-    if dev is None or dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
+    if dev is None:
+        return fn(*args, _stream(stream))
+    s = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        return fn(*args, s)
     with torch.cuda.device(dev):
-        return call(_stream(stream))
+        return fn(*args, s)
 
 
 def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages,
@@ -375,11 +407,11 @@ def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_l
     pages (free_pages [F], free_count [1]). result [2]: pages left, status (0: built; else
     1 too few pages | 2 a sequence past W pages | 4 more tokens than slots, nothing written)."""
     lib = load()
-    tables = (input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages, free_count)
-    dev = _device_of(tables)
-    d = [None if t is None else ctypes.byref(describe(t, QG.I32 if i == 1 and t.dtype == torch.int32 else _u32(t)))
-         for i, t in enumerate(tables)]
-    st = _on(dev, stream, lambda s: lib.tables_ragged_paged(*d, int(page_size), s))
+    dev = _device_of((input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages, free_count))
+    u32 = _TABLE_DTYPE
+    st = _launch(lib.tables_ragged_paged, dev, stream, _record(input_row_offsets, u32), _record(slot_map),
+                 _record(page_table, u32), _record(result, u32), _record(cache_lengths, u32), _record(new_lengths, u32),
+                 _record(free_pages, u32), _record(free_count, u32), page_size)
     if raise_on_error:
         _check(st)
     return st
@@ -401,16 +433,26 @@ def attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, 
     tensor of attention_ragged_paged_workspace(...) elements."""
     lib = load()
     dev = _device_of((out, q, input_row_offsets, kv_blocks, cache_lengths, page_table, kv_scales, workspace))
-    batch = input_row_offsets.shape[0] - 1 if input_row_offsets is not None and input_row_offsets.dim() == 1 else 0
-    for t, shape in ((cache_lengths, (batch,)), (page_table, (batch, page_table.shape[-1] if page_table is not None and page_table.dim() else 0))):
-        if t is not None and (t.dtype not in (torch.int32, torch.uint32) or tuple(t.shape) != shape
-                              or not t.is_contiguous()):
-            raise ValueError("cache_lengths [B] and page_table [B, max_pages] must be contiguous int32 or uint32 tensors")
-    kv = _paged_kv(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity)
-    st = _on(dev, stream, lambda s: lib.attention_ragged_paged(
-        ctypes.byref(describe(out)), ctypes.byref(describe(q)),
-        ctypes.byref(describe(input_row_offsets, _u32(input_row_offsets))), ctypes.byref(kv), int(layer_idx),
-        float(scale), int(bool(causal)), int(window), ctypes.byref(describe(workspace)), s))
+    kv = None
+    if kv_blocks is not None:
+        # the C ABI takes these two by address alone, so their form is checked here
+        batch = input_row_offsets.shape[0] - 1 if input_row_offsets is not None and input_row_offsets.dim() == 1 else -1
+        pages = 0
+        if page_table is not None:
+            if page_table.dim() != 2 or (batch >= 0 and page_table.shape[0] != batch):
+                raise ValueError("page_table must be [B, max_pages]")
+            pages = page_table.shape[1]
+        if cache_lengths is not None and (cache_lengths.dim() != 1 or (batch >= 0 and cache_lengths.shape[0] != batch)):
+            raise ValueError("cache_lengths must be [B]")
+        for t in (cache_lengths, page_table):
+            if t is not None and (t.dtype not in _TABLE_DTYPE or not t.is_contiguous()):
+                raise ValueError("cache_lengths and page_table must be contiguous int32 or uint32 tensors")
+        kv = (_record(kv_blocks, _CACHE_DTYPE)
+              + _KV_TABLES(0 if cache_lengths is None else cache_lengths.data_ptr(),
+                           0 if page_table is None else page_table.data_ptr(), pages)
+              + (_NO_TENSOR if kv_scales is None else _record(kv_scales)) + _KV_GRANULARITY(quantization_granularity))
+    st = _launch(lib.attention_ragged_paged, dev, stream, _record(out), _record(q), _record(input_row_offsets, _TABLE_DTYPE),
+                 kv, layer_idx, scale, 1 if causal else 0, window, _record(workspace))
     if raise_on_error:
         _check(st)
     return st
