@@ -24,7 +24,8 @@ typedef int i32x2v_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kAttnAlign = 32;   // a tile's first position is rounded down to this
+constexpr int kAttnAlign = 64;   // a tile's first position is rounded down to this
+constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row's reference
 
 // What one workgroup works on.
 struct AttnItem {
@@ -35,7 +36,59 @@ struct AttnItem {
   int nsplit;       // chunks reserved per tile of this sequence
   int chunk;        // positions per chunk
   int row0, fresh, cached;   // the sequence's first row of q, new tokens, history
+  int record;       // place of (b, tile) among the tiles that are cut
 };
+
+// What is the same in every lane, as the compiler cannot know where it comes from
+// LDS or through a call.
+__device__ __forceinline__ AttnItem uniform(AttnItem it) {
+  it.b = __builtin_amdgcn_readfirstlane(it.b);
+  it.tile = __builtin_amdgcn_readfirstlane(it.tile);
+  it.split = __builtin_amdgcn_readfirstlane(it.split);
+  it.slots = __builtin_amdgcn_readfirstlane(it.slots);
+  it.nsplit = __builtin_amdgcn_readfirstlane(it.nsplit);
+  it.chunk = __builtin_amdgcn_readfirstlane(it.chunk);
+  it.row0 = __builtin_amdgcn_readfirstlane(it.row0);
+  it.fresh = __builtin_amdgcn_readfirstlane(it.fresh);
+  it.cached = __builtin_amdgcn_readfirstlane(it.cached);
+  it.record = __builtin_amdgcn_readfirstlane(it.record);
+  return it;
+}
+template <typename T>
+__device__ __forceinline__ T* uniform(T* x) {
+  const uint64_t a = reinterpret_cast<uint64_t>(x);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return reinterpret_cast<T*>((uint64_t)hi << 32 | lo);
+}
+// A condition that is the same in every lane, as a scalar one: an MFMA ignores the
+// EXEC mask, so one that is meant to be skipped must be branched around.
+__device__ __forceinline__ bool uniform(bool x) { return __builtin_amdgcn_readfirstlane((int)x) != 0; }
+
+// The kernel's arguments, read again from where it got them, by scalar loads: for
+// a function that is called, not inlined (a copy of them to pass would be written
+// to memory by every lane, and what is loaded through an ordinary pointer would
+// not count as the same in every lane).
+typedef const __attribute__((address_space(4))) uint32_t* kernarg_t;
+__device__ __forceinline__ AttnArgs reload_args(kernarg_t at) {
+  static_assert(sizeof(AttnArgs) % 4 == 0, "whole words");
+  const uint64_t a = (uint64_t)at;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  const kernarg_t from = (kernarg_t)((uint64_t)hi << 32 | lo);
+  AttnArgs p;
+  uint32_t w[sizeof(AttnArgs) / 4];
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(AttnArgs) / 4); ++i) w[i] = from[i];
+  __builtin_memcpy(&p, w, sizeof(p));
+  return p;
+}
+
+// The workspace: a count of cut tiles (of sequences with more than one chunk), a
+// record for each, then the slots. The launch that computes them writes the count
+// and the records, the one that joins the chunks reads them.
+constexpr int kRecordInts = 16;
+constexpr long long attn_header_floats(int target) { return (long long)kRecordInts * (target + 2); }
+// Floats of a slot: the rows' outputs, then their maxima and sums.
+__host__ __device__ constexpr long long attn_slot_floats(int bm, int dp) { return (long long)bm * (dp + 2); }
 
 // Tiles of a sequence, and the positions its longest tile may cover.
 __device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh, int bm) {
@@ -51,15 +104,16 @@ __device__ __forceinline__ int attn_span(const AttnArgs& p, int len, int bm) {
 template <int NT>
 struct AttnScan {
   unsigned long long cost[NT / 64];
-  int items[NT / 64], slots[NT / 64];
+  int items[NT / 64], slots[NT / 64], cuts[NT / 64];
   AttnItem found;
 };
 
-// Item `want` of the launch (COUNT_SPLIT: among the tiles that are cut, one item
-// per tile; `split` is then 0). All NT threads call it. Items are ordered by
-// sequence, then chunk, then tile.
-template <int NT, bool COUNT_SPLIT>
-__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
+// Item blockIdx.x / hkv of the launch; all NT threads call it. Items are ordered by
+// sequence, then chunk, then tile (the last tiles, which see the most positions,
+// first). Workgroup 0 also writes the workspace's count of cut tiles.
+template <int NT>
+__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, AttnScan<NT>& sh) {
+  const int want = blockIdx.x / p.hkv;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   unsigned long long cost = 0;
   int row00 = 0, fresh0 = 0, len0 = 0;
@@ -84,7 +138,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
   int chunk = even < (unsigned long long)p.min_chunk ? p.min_chunk : even > INT32_MAX / 2 ? INT32_MAX / 2 : (int)even;
   chunk = (chunk + p.step - 1) / p.step * p.step;
 
-  int base = 0, slot_base = 0;
+  int base = 0, slot_base = 0, cut_base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
     int tiles = 0, ns = 0, row0 = row00, fresh = fresh0, len = len0;
@@ -97,42 +151,36 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
       tiles = attn_tiles(p, fresh, p.bm);
       if (tiles) ns = (attn_span(p, len, p.bm) + chunk - 1) / chunk;
     }
-    const int items = COUNT_SPLIT ? (ns > 1 ? tiles : 0) : tiles * ns;
-    const int slots = ns > 1 ? tiles * ns * p.hkv : 0;
-    int ii = items, is = slots;
+    const int items = tiles * ns, cuts = ns > 1 ? tiles : 0, slots = cuts * ns * p.hkv;
+    int ii = items, is = slots, ic = cuts;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int vi = __shfl_up(ii, d), vs = __shfl_up(is, d);
-      if (lane >= d) { ii += vi; is += vs; }
+      const int vi = __shfl_up(ii, d), vs = __shfl_up(is, d), vc = __shfl_up(ic, d);
+      if (lane >= d) { ii += vi; is += vs; ic += vc; }
     }
-    if (lane == 63) { sh.items[wave] = ii; sh.slots[wave] = is; }
+    if (lane == 63) { sh.items[wave] = ii; sh.slots[wave] = is; sh.cuts[wave] = ic; }
     __syncthreads();
-    int bi = base, bs = slot_base;
+    int bi = base, bs = slot_base, bc = cut_base;
 #pragma unroll
     for (int w = 0; w < NT / 64; ++w) {
-      if (w < wave) { bi += sh.items[w]; bs += sh.slots[w]; }
+      if (w < wave) { bi += sh.items[w]; bs += sh.slots[w]; bc += sh.cuts[w]; }
       base += sh.items[w];
       slot_base += sh.slots[w];
+      cut_base += sh.cuts[w];
     }
     const int first = bi + ii - items;
     if (want >= first && want < bi + ii) {
-      const int local = want - first;
-      // the last tiles, which see the most positions, first
-      sh.found = AttnItem{b, tiles - 1 - local % tiles, local / tiles, bs + is - slots, ns, chunk, row0, fresh, len - fresh};
+      const int local = want - first, tile = tiles - 1 - local % tiles;
+      sh.found = AttnItem{b, tile, local / tiles, bs + is - slots, ns, chunk, row0, fresh, len - fresh, bc + ic - cuts + tile};
     }
     __syncthreads();
-    if (want < base) break;
+    if (want < base && blockIdx.x > 0) break;
   }
-  AttnItem it = sh.found;
-  it.b = __builtin_amdgcn_readfirstlane(it.b);
-  it.tile = __builtin_amdgcn_readfirstlane(it.tile);
-  it.split = __builtin_amdgcn_readfirstlane(it.split);
-  it.slots = __builtin_amdgcn_readfirstlane(it.slots);
-  it.nsplit = __builtin_amdgcn_readfirstlane(it.nsplit);
-  it.chunk = __builtin_amdgcn_readfirstlane(it.chunk);
-  it.row0 = __builtin_amdgcn_readfirstlane(it.row0);
-  it.fresh = __builtin_amdgcn_readfirstlane(it.fresh);
-  it.cached = __builtin_amdgcn_readfirstlane(it.cached);
+  if (blockIdx.x == 0 && tid == 0) reinterpret_cast<int*>(p.workspace)[0] = cut_base;
+  const AttnItem it = uniform(sh.found);
+  // one workgroup per cut tile describes it for the join
+  if (it.b >= 0 && it.nsplit > 1 && it.split == 0 && blockIdx.x % p.hkv == 0 && tid == 0)
+    *reinterpret_cast<AttnItem*>(p.workspace + (size_t)kRecordInts * (it.record + 1)) = it;
   return it;
 }
 
@@ -193,8 +241,9 @@ __device__ __forceinline__ void wait_loads() {
 // until this wave's LDS reads have returned (before a load into the same place)
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
+// LDS byte address, the same in every lane
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
 }
 
 // the larger of x and the other half-wave's x
@@ -220,10 +269,22 @@ __device__ __forceinline__ uint64_t lds_read_tr8(const void* p) {
                                           (__attribute__((address_space(3))) i32x2v_t*)(const_cast<void*>(p))));
 }
 
-// Floats of a workspace slot: the rows' outputs, then their maxima and sums.
-__host__ __device__ constexpr long long attn_slot_floats(int bm, int dp) { return (long long)bm * (dp + 2); }
+// The pages of a tile's positions where page_size is a multiple of 16: 16 aligned
+// positions lie in one page, whose id is a scalar load.
+typedef const __attribute__((address_space(4))) uint32_t* page_list_t;
+struct Row16 {
+  size_t row;    // cache row (page, slot) of the first of 16 positions
+  int pos;       // that position
+};
+// of positions pos0 .. pos0 + 15, or where all of these lie outside [begin, end) of 16
+// others that do not (their pages may not exist)
+__device__ __forceinline__ Row16 rows_of16(const AttnArgs& p, page_list_t pages, int pos0, int begin, int end) {
+  const int x = min(max(pos0, begin & ~15), (end - 1) & ~15);
+  const uint32_t pg = fast_div(x, p.div_mul, p.div_shift);
+  return Row16{(size_t)pages[pg] * p.page_size + (x - pg * p.page_size), x};
+}
 
-hipError_t launch_attention_rows(AttnArgs p, int mt, hipStream_t stream);
-hipError_t launch_attention_tiles(AttnArgs p, hipStream_t stream);
+hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
+hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
 
 }  // namespace qg

@@ -9,6 +9,8 @@
 // It is a second launch on the same stream rather than the task of the last
 // chunk to finish: that needs counters which every call must find at zero, and
 // ordering between the XCDs' caches within a kernel.
+#include <algorithm>
+
 #include "attention_common.h"
 
 namespace qg {
@@ -16,30 +18,28 @@ namespace qg {
 namespace {
 
 constexpr int JT = 256;
-constexpr int kRowsTarget = 1024, kRowsMinChunk = 512, kRowsStep = 128;
-constexpr int kTileTarget = 512, kTileMinChunk = 512, kTileStep = 64;
+constexpr int kRowsTarget = 1024, kRowsMinChunk = 128, kRowsStep = 128;
+constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 }  // namespace
 
-// WPR waves share a row's chunks (4 where rows are few and chunks many).
+// WPR waves share a row's chunks (4 where rows are few, 1 else).
 template <int DP, int WPR>
-__global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int rows_per_wg) {
+__global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int parts, int rows_per_wg) {
   constexpr int VL = DP / 64;   // floats per lane
-  __shared__ AttnScan<JT> scan;
   __shared__ float part[WPR > 1 ? 4 : 1][DP + 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int parts = (p.bm + rows_per_wg - 1) / rows_per_wg;
   const int h = blockIdx.x % p.hkv, at = blockIdx.x / p.hkv;
-  const AttnItem it = attn_locate<JT, true>(p, at / parts, scan);
-  if (it.b < 0) return;
+  if (at / parts >= reinterpret_cast<const int*>(p.workspace)[0]) return;
+  const AttnItem it = *reinterpret_cast<const AttnItem*>(p.workspace + (size_t)kRecordInts * (at / parts + 1));
   const AttnTile t = attn_tile(p, it);
   const int ns = (t.end - t.start + it.chunk - 1) / it.chunk;
   if (ns <= 1) return;   // written by its only chunk
   const long long slot_floats = attn_slot_floats(p.bm, DP);
-  const float* ws = p.workspace + (it.slots + (long long)(it.tile * p.hkv + h) * it.nsplit) * slot_floats;
+  const float* ws = p.workspace + attn_header_floats(p.target) + (it.slots + (long long)(it.tile * p.hkv + h) * it.nsplit) * slot_floats;
   const int r0 = at % parts * rows_per_wg, r1 = min(t.r_count, r0 + rows_per_wg);
   for (int r = r0 + (WPR > 1 ? 0 : wave); r < r1; r += WPR > 1 ? 1 : 4) {
     const float* ml = ws + p.bm * DP + 2 * r;
@@ -95,15 +95,18 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int rows
   }
 }
 
-static hipError_t launch_join(const AttnArgs& p, int rows_per_wg, hipStream_t stream) {
-  // tiles that are cut: at least two slots each, of fewer than 2 target
-  const long long tiles = min((long long)(p.T * p.group / p.bm + p.batch), (long long)(p.target / p.hkv + 1));
-  const long long parts = (p.bm + rows_per_wg - 1) / rows_per_wg;
-  const dim3 grid((unsigned)(tiles * parts * p.hkv));
-#define QG_JOIN(DP)                                                                              \
-  do {                                                                                           \
-    if (rows_per_wg == 1) attention_join_kernel<DP, 4><<<grid, JT, 0, stream>>>(p, rows_per_wg); \
-    else attention_join_kernel<DP, 1><<<grid, JT, 0, stream>>>(p, rows_per_wg);                  \
+static hipError_t launch_join(const AttnArgs& p, long long tiles, hipStream_t stream) {
+  // tiles that are cut have at least two slots each, of fewer than 2 target
+  const long long cut = std::min(tiles, (long long)(p.target / p.hkv + 1));
+  const long long rows = std::min<long long>(p.bm, p.T * p.group);
+  const bool few = cut * p.hkv * rows <= 8 * p.num_cus;
+  const int per_wg = few ? 1 : 16;
+  const long long parts = (rows + per_wg - 1) / per_wg;
+  const dim3 grid((unsigned)(cut * parts * p.hkv));
+#define QG_JOIN(DP)                                                                                 \
+  do {                                                                                              \
+    if (few) attention_join_kernel<DP, 4><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);          \
+    else attention_join_kernel<DP, 1><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);              \
   } while (0)
   if (p.d <= 64) QG_JOIN(64);
   else if (p.d <= 128) QG_JOIN(128);
@@ -114,9 +117,9 @@ static hipError_t launch_join(const AttnArgs& p, int rows_per_wg, hipStream_t st
 
 int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t hkv, int64_t d) {
   (void)T; (void)batch; (void)hq;
-  const int64_t rows_target = kRowsTarget > hkv ? kRowsTarget : hkv, tile_target = kTileTarget > hkv ? kTileTarget : hkv;
-  const int64_t rows = 2 * rows_target * attn_slot_floats(32, dp_of(d)), tile = 2 * tile_target * attn_slot_floats(128, dp_of(d));
-  return rows > tile ? rows : tile;
+  const int64_t rt = std::max<int64_t>(kRowsTarget, hkv), tt = std::max<int64_t>(kTileTarget, hkv);
+  return std::max(attn_header_floats((int)rt) + 2 * rt * attn_slot_floats(32, dp_of(d)),
+                  attn_header_floats((int)tt) + 2 * tt * attn_slot_floats(128, dp_of(d)));
 }
 
 hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
@@ -130,13 +133,20 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   const bool few = rows <= 32LL * p.batch;
   const int mt = rows > 16LL * p.batch ? 2 : 1;
   p.bm = few ? 16 * mt : 128;
-  p.target = few ? kRowsTarget : kTileTarget;
-  if (p.target < p.hkv) p.target = p.hkv;
+  p.target = std::max(few ? kRowsTarget : kTileTarget, p.hkv);
   p.min_chunk = few ? kRowsMinChunk : kTileMinChunk;
   p.step = few ? kRowsStep : kTileStep;
-  const hipError_t e = few ? launch_attention_rows(p, mt, stream) : launch_attention_tiles(p, stream);
-  if (e != hipSuccess || p.max_pages * p.page_size <= p.min_chunk) return e;   // nothing can be cut
-  return launch_join(p, few ? 1 : 16, stream);
+  // Sequence b has ceil(new_b * group / bm) tiles per key/value head. Items: at most
+  // target / hkv + tiles (a chunk is at least the work over the target), and each tile
+  // has as many as the page table has room for. Workgroups past the last item return.
+  const long long tiles = rows / p.bm + p.batch;
+  const long long room = (p.max_pages * p.page_size + p.min_chunk - 1) / p.min_chunk;
+  const long long items = std::min(tiles + p.target / p.hkv + 1, room < tiles + p.target ? tiles * room : (long long)INT64_MAX);
+  if (items * p.hkv > INT32_MAX) return hipErrorNotSupported;
+  const unsigned grid = (unsigned)(items * p.hkv);
+  const hipError_t e = few ? launch_attention_rows(p, mt, grid, stream) : launch_attention_tiles(p, grid, stream);
+  if (e != hipSuccess || room <= 1) return e;   // nothing can be cut
+  return launch_join(p, tiles, stream);
 }
 
 }  // namespace qg

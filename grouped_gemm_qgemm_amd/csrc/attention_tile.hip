@@ -37,7 +37,6 @@ namespace {
 
 constexpr int AW = 4;                // waves
 constexpr int TPG = 1024;            // page table entries held in LDS at a time
-constexpr float kSlack = 8.f;        // log2 of how far a weight may exceed its reference
 
 // 16-byte chunk c of LDS row r (DP bf16 elements): the 16 rows of a read phase of
 // the key fragments, and the 4 x 64 bytes of a transposed read of values, meet
@@ -261,8 +260,8 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             for (int rt = 0; rt < RT; ++rt) sc[rt][nb] = part[rt];
           }
         }
-        const bool masked = (p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
-                            k0 + KB > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end);
+        const bool masked = uniform((p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
+                                    k0 + KB > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end));
         if (masked) {
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
@@ -404,7 +403,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   }
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
-  float* ws = p.workspace + (size_t)slot * attn_slot_floats(p.bm, DP);
+  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(p.bm, DP);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const float sum = l[rt] + __shfl_xor(l[rt], 32);
@@ -439,30 +438,24 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   return false;
 }
 
-// Called, not inlined: hardly ever taken, and its registers stay out of the
-// kernel's. The arguments are read again where the kernel got them, since a copy
-// of them to pass would be written to memory by every lane.
+// Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
 template <int DP, int GRAN, int RT>
-__device__ __attribute__((noinline)) void attend_tile_safe(const AttnArgs* p, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
-  attend_tile<DP, GRAN, RT, true>(*p, it, blockIdx.x % p->hkv, *lds);
+__device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
+  const AttnArgs p = reload_args(args);
+  attend_tile<DP, GRAN, RT, true>(p, uniform(it), blockIdx.x % p.hkv, *lds);
 }
 
 template <int DP, int GRAN, int RT>
 __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
   __shared__ AttnTileLds<DP, GRAN> lds;
   const int h = blockIdx.x % p.hkv;
-  const AttnItem it = attn_locate<AW * 64, false>(p, blockIdx.x / p.hkv, lds.scan);
+  const AttnItem it = attn_locate<AW * 64>(p, lds.scan);
   if (it.b < 0) return;
   if (attend_tile<DP, GRAN, RT, false>(p, it, h, lds))
-    attend_tile_safe<DP, GRAN, RT>((const AttnArgs*)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
+    attend_tile_safe<DP, GRAN, RT>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
 }
 
-hipError_t launch_attention_tiles(AttnArgs p, hipStream_t stream) {
-  const long long tiles = p.T * p.group / p.bm + p.batch;
-  // items: at most target + tiles (a chunk is at least the work over the target)
-  const long long items = tiles + p.target / p.hkv + 1;
-  if (items * p.hkv > INT32_MAX) return hipErrorNotSupported;
-  const dim3 grid((unsigned)(items * p.hkv));
+hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream) {
 #define QG_ATTN(DP, GRAN) attention_tile_kernel<DP, GRAN, 1><<<grid, AW * 64, 0, stream>>>(p)
   const int gran = p.fp8 ? p.gran : 0;
   if (p.d <= 64) {
