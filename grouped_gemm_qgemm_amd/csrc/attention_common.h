@@ -2,17 +2,25 @@
 // into items, e4m3 conversion, addresses of cache rows.
 //
 // A tile is BM consecutive (token, query head) rows of one sequence and one
-// key/value head. Its positions are cut into chunks, one work item each; tiles
-// of more than one chunk leave partial results in the workspace, which a second
-// kernel joins. Only the device knows the lengths, so every workgroup derives
-// the cut from them: with W the sum over the tiles of the positions they cover,
+// key/value head. Only the device knows the lengths, so every workgroup derives
+// its share of the work from them, in one of two ways:
+//
+// Items (many rows): a tile's positions are cut into chunks, one item each, with W
+// the sum over the tiles of the positions they cover:
 //
 //   chunk = max(min_chunk, W / target) rounded up to the kernel's step
 //
-// which gives about target + tiles items of nearly equal size, whatever the mix
-// of lengths. A tile that is cut has fewer than 2 * positions / chunk items, so
-// all of them together have fewer than 2 * target: the workspace does not depend
-// on the batch or the lengths.
+// which gives about target + tiles items. A tile that is cut has fewer than
+// 2 * positions / chunk items, so all of them together have fewer than 2 * target.
+//
+// Shares (few rows): the positions of all tiles, in units of `step`, form one line
+// that is cut into `target / hkv` pieces of equal length, one per workgroup (and
+// head). A piece may hold the end of one tile, whole tiles, and the start of
+// another, so every workgroup has the same amount to read, whatever the lengths.
+//
+// What a workgroup computes of a cut tile goes to the workspace, as does a record
+// of the tile; a second launch joins the parts. Neither the parts nor the records
+// grow with the batch or the lengths.
 #pragma once
 
 #include "device_common.h"
@@ -36,7 +44,15 @@ struct AttnItem {
   int nsplit;       // chunks reserved per tile of this sequence
   int chunk;        // positions per chunk
   int row0, fresh, cached;   // the sequence's first row of q, new tokens, history
-  int record;       // place of (b, tile) among the tiles that are cut
+  int record;       // place of (b, tile) among the tiles of sequences with more than one chunk
+};
+
+// A cut tile, for the join: its rows, and where its parts lie. Part 0 of head h is
+// slot first + h * head_step, part s > 0 slot next + (s - 1) * step + h * head_step.
+struct AttnRecord {
+  int parts;             // nothing to join below 2
+  int row0, r_first, r_count;
+  int first, next, step, head_step;
 };
 
 // What is the same in every lane, as the compiler cannot know where it comes from
@@ -82,13 +98,16 @@ __device__ __forceinline__ AttnArgs reload_args(kernarg_t at) {
   return p;
 }
 
-// The workspace: a count of cut tiles (of sequences with more than one chunk), a
-// record for each, then the slots. The launch that computes them writes the count
-// and the records, the one that joins the chunks reads them.
-constexpr int kRecordInts = 16;
-constexpr long long attn_header_floats(int target) { return (long long)kRecordInts * (target + 2); }
-// Floats of a slot: the rows' outputs, then their maxima and sums.
+// The workspace: a count of records, the records, the slots. A slot holds a part's
+// output rows, then their maxima and sums.
+constexpr int kRecordInts = 8;
+static_assert(sizeof(AttnRecord) == kRecordInts * 4, "a record's place in the workspace");
+__host__ __device__ constexpr long long attn_header_floats(int target) { return (long long)kRecordInts * (target + 16); }
 __host__ __device__ constexpr long long attn_slot_floats(int bm, int dp) { return (long long)bm * (dp + 2); }
+__device__ __forceinline__ int* attn_record_count(const AttnArgs& p) { return reinterpret_cast<int*>(p.workspace); }
+__device__ __forceinline__ AttnRecord* attn_record(const AttnArgs& p, int i) {
+  return reinterpret_cast<AttnRecord*>(p.workspace + (size_t)kRecordInts * (i + 1));
+}
 
 // Tiles of a sequence, and the positions its longest tile may cover.
 __device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh, int bm) {
@@ -108,12 +127,11 @@ struct AttnScan {
   AttnItem found;
 };
 
-// Item blockIdx.x / hkv of the launch; all NT threads call it. Items are ordered by
-// sequence, then chunk, then tile (the last tiles, which see the most positions,
-// first). Workgroup 0 also writes the workspace's count of cut tiles.
+// Item `want` of the launch, for head h; all NT threads call it. Items are ordered
+// by sequence, then chunk, then tile (the last tiles, which see the most positions,
+// first). Workgroup 0 also writes the workspace's count of records.
 template <int NT>
-__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, AttnScan<NT>& sh) {
-  const int want = blockIdx.x / p.hkv;
+__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int h, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   unsigned long long cost = 0;
   int row00 = 0, fresh0 = 0, len0 = 0;
@@ -178,9 +196,6 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, AttnScan<NT>&
   }
   if (blockIdx.x == 0 && tid == 0) reinterpret_cast<int*>(p.workspace)[0] = cut_base;
   const AttnItem it = uniform(sh.found);
-  // one workgroup per cut tile describes it for the join
-  if (it.b >= 0 && it.nsplit > 1 && it.split == 0 && blockIdx.x % p.hkv == 0 && tid == 0)
-    *reinterpret_cast<AttnItem*>(p.workspace + (size_t)kRecordInts * (it.record + 1)) = it;
   return it;
 }
 
@@ -202,6 +217,106 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem&
   t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
   t.start = t.begin / kAttnAlign * kAttnAlign;
   return t;
+}
+
+// The share of workgroup w (of a head): units [at, end) of the line, of which `at` is
+// unit `in_tile` of tile `tile` of sequence b. The line has `units` units in all and
+// `pieces` shares; b is -1 where the share is empty.
+struct AttnShare {
+  long long units, at, end;
+  int pieces, b, tile, in_tile;
+  int row0, fresh, cached;    // of sequence b
+};
+__device__ __forceinline__ long long share_start(long long units, int pieces, int w) { return units * w / pieces; }
+// the workgroup whose share holds unit u
+__device__ __forceinline__ int share_of(long long units, int pieces, long long u) {
+  return (int)(((u + 1) * pieces + units - 1) / units) - 1;
+}
+// units of each tile of a sequence
+__device__ __forceinline__ int attn_units(const AttnArgs& p, int len) { return (attn_span(p, len, p.bm) + p.step - 1) / p.step; }
+
+template <int NT>
+struct ShareScan {
+  long long part[NT / 64];
+  AttnShare found;
+};
+
+template <int NT>
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, int w, ShareScan<NT>& sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  long long mine = 0;
+  int row00 = 0, fresh0 = 0, len0 = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += NT) {
+    const int b = b0 + tid;
+    if (b < p.batch) {
+      const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
+      const int len = fresh + (int)p.cache_len[b];
+      if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
+      mine += (long long)attn_tiles(p, fresh, p.bm) * attn_units(p, len);
+    }
+  }
+  const long long first_mine = mine;   // of sequence tid, where the batch has at most NT
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) mine += __shfl_xor(mine, d);
+  if (lane == 0) sh.part[wave] = mine;
+  if (tid == 0) sh.found.b = -1;
+  __syncthreads();
+  AttnShare s{};
+#pragma unroll
+  for (int v = 0; v < NT / 64; ++v) s.units += sh.part[v];
+  s.pieces = (int)min((long long)max(p.target / p.hkv, 1), s.units);
+  if (w >= s.pieces) {
+    s.b = -1;
+    return s;
+  }
+  s.at = share_start(s.units, s.pieces, w);
+  s.end = share_start(s.units, s.pieces, w + 1);
+  long long base = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += NT) {
+    const int b = b0 + tid;
+    int row0 = row00, fresh = fresh0, len = len0;
+    long long units = b0 == 0 && p.batch <= NT ? first_mine : 0;
+    if (p.batch > NT && b < p.batch) {
+      row0 = (int)p.offs[b];
+      fresh = (int)p.offs[b + 1] - row0;
+      len = fresh + (int)p.cache_len[b];
+      units = (long long)attn_tiles(p, fresh, p.bm) * attn_units(p, len);
+    }
+    long long incl = units;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const long long v = __shfl_up(incl, d);
+      if (lane >= d) incl += v;
+    }
+    __syncthreads();
+    if (lane == 63) sh.part[wave] = incl;
+    __syncthreads();
+    long long before = base;
+#pragma unroll
+    for (int v = 0; v < NT / 64; ++v) {
+      if (v < wave) before += sh.part[v];
+      base += sh.part[v];
+    }
+    const long long first = before + incl - units;
+    if (s.at >= first && s.at < before + incl) {
+      const int un = attn_units(p, len), local = (int)(s.at - first);
+      sh.found.b = b;
+      sh.found.tile = local / un;
+      sh.found.in_tile = local % un;
+      sh.found.row0 = row0;
+      sh.found.fresh = fresh;
+      sh.found.cached = len - fresh;
+    }
+    __syncthreads();
+    if (s.at < base) break;
+  }
+  s.b = __builtin_amdgcn_readfirstlane(sh.found.b);
+  s.tile = __builtin_amdgcn_readfirstlane(sh.found.tile);
+  s.in_tile = __builtin_amdgcn_readfirstlane(sh.found.in_tile);
+  s.row0 = __builtin_amdgcn_readfirstlane(sh.found.row0);
+  s.fresh = __builtin_amdgcn_readfirstlane(sh.found.fresh);
+  s.cached = __builtin_amdgcn_readfirstlane(sh.found.cached);
+  return s;
 }
 
 // x / d for the divisor that (mul, shift) were made for; x < 2^31
@@ -241,9 +356,10 @@ __device__ __forceinline__ void wait_loads() {
 // until this wave's LDS reads have returned (before a load into the same place)
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// LDS byte address, the same in every lane
+// LDS byte address, the same in every lane: the low half of a generic pointer into
+// LDS (a cast of the pointer itself would first test it for null)
 __device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p);
+  return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(p));
 }
 
 // the larger of x and the other half-wave's x
@@ -284,6 +400,8 @@ __device__ __forceinline__ Row16 rows_of16(const AttnArgs& p, page_list_t pages,
   return Row16{(size_t)pages[pg] * p.page_size + (x - pg * p.page_size), x};
 }
 
+// Shares per launch (over all heads) that run at once: `target` for launch_attention_rows.
+int attention_rows_resident(const AttnArgs& p, int mt);
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
 

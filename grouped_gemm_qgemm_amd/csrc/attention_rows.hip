@@ -1,8 +1,8 @@
 // Attention over the paged cache for few rows per key/value head (single tokens,
 // drafted tokens): a stream over the cache, bound by HBM.
 //
-// A tile is 16 * MT (token, query head) rows. A workgroup takes one chunk of one
-// tile's positions; its waves take blocks of 32 positions in turn, each with its
+// A tile is 16 * MT (token, query head) rows. A workgroup takes an equal share of
+// all tiles' positions, part by part; its waves take blocks of 32 positions in turn, each with its
 // own ring of two blocks in LDS, filled by direct-to-LDS loads (no registers
 // held, no barrier between the waves). Scores come transposed from 16x16x32
 // MFMAs, S^T = K Q^T: a lane holds eight scores of one row, and they are, as they
@@ -15,6 +15,8 @@
 //
 // Running maximum, e4m3 scales and what a row must not see are dealt with as in
 // the kernel for many rows.
+#include <algorithm>
+
 #include "attention_common.h"
 
 namespace qg {
@@ -33,24 +35,37 @@ __device__ __forceinline__ int swz_r(int r) {
   return CH >= 16 ? (r & 7) | ((r >> 4) & 1) << 3 : CH == 8 ? ((r >> 1) & 3) | ((r >> 4) & 1) << 2 : ((r >> 2) & 1) | ((r >> 4) & 1) << 1;
 }
 
-template <int DP, int GRAN, int MT, int NW>
+// until the loads of at most min(left, N) blocks of LB loads each are in flight
+template <int LB, int N>
+__device__ __forceinline__ void wait_blocks(int left) {
+  if constexpr (N == 0) {
+    wait_loads<0>();
+  } else {
+    if (left >= N) wait_loads<N * LB>();
+    else wait_blocks<LB, N - 1>(left);
+  }
+}
+
+template <int DP, int GRAN, int MT, int NW, int NST>
 struct AttnRowsLds {
   static constexpr int TILE = 2 * DP * (GRAN > 0 ? 1 : 2);   // 16-byte chunks of a block's keys (or values)
   static constexpr int R = GRAN > 0 ? DP / GRAN : 1;          // scale runs per head, at most
-  __attribute__((aligned(16))) u32x4_t ring[NW][2][2][TILE];      // [wave][block parity][keys, values]
-  __attribute__((aligned(16))) float ring_s[GRAN > 0 ? NW : 1][2][R][2][32];   // run scales [run][keys, values][position]
+  __attribute__((aligned(16))) u32x4_t ring[NW][NST][2][TILE];    // [wave][slot][keys, values]
+  __attribute__((aligned(16))) float ring_s[GRAN > 0 ? NW : 1][NST][R][2][32];   // run scales [run][keys, values][position]
   uint32_t pages[RPG];
   float w_m[NW][16 * MT], w_l[NW][16 * MT];
-  AttnScan<NW * 64> scan;
+  ShareScan<NW * 64> scan;
 };
 
 }  // namespace
 
-// One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
-// values are selected per token. Without it, returns whether some output came out
+// Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1
+// and go to that slot of the workspace else. GRAN: head-dim elements per scale of an
+// e4m3 cache, 0 for bf16. SAFE: values are selected per token. Without it, returns whether some output came out
 // as an infinity or NaN, for the whole workgroup, and then has written nothing.
-template <int DP, int GRAN, int MT, int NW, bool SAFE>
-__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, AttnRowsLds<DP, GRAN, MT, NW>& lds) {
+template <int DP, int GRAN, int MT, int NW, int NST, bool SAFE>
+__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h, int c_first, int c_end, int slot,
+                                            AttnRowsLds<DP, GRAN, MT, NW, NST>& lds) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int ES = FP8 ? 1 : 2;              // bytes per cached element
   constexpr int CH = DP * ES / 16;             // chunks per LDS row
@@ -62,20 +77,17 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
   constexpr int RS = FP8 ? GRAN / 32 : NS;     // MFMA steps per run
   constexpr int NT = NW * 64;
   // floats per row of a wave's partial output in LDS
-  constexpr int OS = 16 * MT * (DP + 4) * 4 <= 4 * TILE * 16 ? DP + 4 : DP;
-  static_assert(16 * MT * OS * 4 <= 4 * TILE * 16, "a wave's partial output fits its ring");
+  constexpr int OS = 16 * MT * (DP + 4) * 4 <= NST * 2 * TILE * 16 ? DP + 4 : DP;
+  static_assert(16 * MT * OS * 4 <= NST * 2 * TILE * 16, "a wave's partial output fits its ring");
   static_assert(LD >= 2, "a load covers 16 positions at most");
+  constexpr int LB = 2 * LD + (FP8 ? R : 0);   // loads per block
+  static_assert((NST - 1) * LB < 64, "loads in flight that a wait can count");
   auto& ring = lds.ring;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, j = lane >> 4;
-  const int h = blockIdx.x % p.hkv;
   const AttnTile t = attn_tile(p, it);
-  const int c_first = t.start + it.split * it.chunk;          // this item's positions [c_first, c_end)
-  const int c_end = min(t.end, c_first + it.chunk);
-  if (c_first >= c_end) return false;                         // the sequence's longer tiles need this chunk
-  const bool alone = t.end - t.start <= it.chunk;
 
   // rows of this lane, one per 16-row tile
   const int rows = it.fresh * p.group;
@@ -98,7 +110,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
   const int chunks = p.d * ES / 16;                           // chunks of a cache row that exist
   // head dims between p.d and DP: never loaded, zero from here on
   if (chunks < CH) {
-    for (int e = tid; e < NW * 4 * TILE; e += NT) (&ring[0][0][0][0])[e] = u32x4_t{0, 0, 0, 0};
+    for (int e = tid; e < NW * NST * 2 * TILE; e += NT) (&ring[0][0][0][0])[e] = u32x4_t{0, 0, 0, 0};
   }
   const float cs = p.scale * kLog2e;
   const uint32_t row_bytes = (uint32_t)(p.hkv * p.d * ES);    // a (page, slot) row
@@ -133,13 +145,13 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n) acc[mt][n] = float4_t{0.f, 0.f, 0.f, 0.f};
   }
   // as many positions at a time as the list of pages covers
-  const int seg = by16 ? it.chunk : (int)min((long long)it.chunk, (long long)(RPG - 1) * p.page_size / (32 * NW) * (32 * NW));
+  const int seg = by16 ? c_end - c_first : (int)min((long long)(c_end - c_first), (long long)(RPG - 1) * p.page_size / (32 * NW) * (32 * NW));
   for (int s_first = c_first; s_first < c_end; s_first += seg) {
     const int s_end = min(c_end, s_first + seg);
     const int page0 = by16 ? 0 : fast_div(max(s_first, t.begin), p.div_mul, p.div_shift);
     if (!by16) {
       const int page1 = fast_div(s_end - 1, p.div_mul, p.div_shift);
-      __syncthreads();
+      if (s_first > c_first) __syncthreads();
       for (int e = tid; e <= page1 - page0; e += NT) lds.pages[e] = my_pages[page0 + e];
     }
     if (!by16 || chunks < CH) __syncthreads();
@@ -205,15 +217,19 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     };
 
     const int blocks = (s_end - s_first + 31) / 32;
-    if (wave < blocks) issue(wave, 0);
-    int at = 0;
-    for (int i = wave; i < blocks; i += NW, at ^= 1) {
-      if (i + NW < blocks) {
-        issue(i + NW, at ^ 1);
-        wait_loads<2 * LD + (FP8 ? R : 0)>();
-      } else {
-        wait_loads<0>();
+    // NST - 1 blocks in flight besides the one in hand
+    const int my_blocks = wave < blocks ? (blocks - wave + NW - 1) / NW : 0;
+#pragma unroll
+    for (int u = 0; u < NST - 1; ++u)
+      if (u < my_blocks) issue(wave + u * NW, u);
+    int at = 0, to = NST - 1;
+    for (int n = 0; n < my_blocks; ++n, at = at + 1 == NST ? 0 : at + 1) {
+      const int i = wave + n * NW;
+      if (n + NST - 1 < my_blocks) {
+        issue(i + (NST - 1) * NW, to);
+        to = to + 1 == NST ? 0 : to + 1;
       }
+      wait_blocks<LB, NST - 1>(my_blocks - 1 - n);
       const int k0 = s_first + 32 * i;
       const u32x4_t* lk = ring[wave][at][0];
       const char* lv = reinterpret_cast<const char*>(ring[wave][at][1]);
@@ -402,8 +418,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n) *reinterpret_cast<float4_t*>(mine + (16 * mt + col) * OS + 16 * n + 4 * j) = acc[mt][n];
   }
   __syncthreads();
-  const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
-  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(16 * MT, DP);
+  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)max(slot, 0) * attn_slot_floats(16 * MT, DP);
   for (int e = tid; e < t.r_count * (DP / 4); e += NT) {
     const int r = e / (DP / 4), d = e % (DP / 4) * 4;
     float top = -INFINITY;
@@ -420,7 +435,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
       sum = __builtin_fmaf(lds.w_l[w][r], f, sum);
     }
-    if (alone) {
+    if (slot < 0) {
       if (d < p.d) {
         const int row = t.r_first + r;
         const float inv = 1.f / sum;   // every row sees a position
@@ -439,44 +454,107 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 }
 
 // Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
-template <int DP, int GRAN, int MT, int NW>
-__device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, AttnRowsLds<DP, GRAN, MT, NW>* lds) {
+template <int DP, int GRAN, int MT, int NW, int NST>
+__device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int c_first, int c_end, int slot,
+                                                           AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_rows<DP, GRAN, MT, NW, true>(p, uniform(it), *lds);
+  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), blockIdx.x / 8 % p.hkv, __builtin_amdgcn_readfirstlane(c_first),
+                                           __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds);
 }
 
-template <int DP, int GRAN, int MT, int NW>
+template <int DP, int GRAN, int MT, int NW, int NST>
 __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) {
-  __shared__ AttnRowsLds<DP, GRAN, MT, NW> lds;
-  const AttnItem it = attn_locate<NW * 64>(p, lds.scan);
-  if (it.b < 0) return;
-  if (attend_rows<DP, GRAN, MT, NW, false>(p, it, lds))
-    attend_rows_safe<DP, GRAN, MT, NW>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
+  __shared__ AttnRowsLds<DP, GRAN, MT, NW, NST> lds;
+  // Workgroups go to the eight XCDs in turn: all heads of a share to one of them, so
+  // that its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
+  const int h = blockIdx.x / 8 % p.hkv, w = blockIdx.x / 8 / p.hkv * 8 + blockIdx.x % 8;
+  AttnShare s = attn_share<NW * 64>(p, w, lds.scan);
+  if (h == 0 && threadIdx.x == 0) {
+    if (w == 0) *attn_record_count(p) = gridDim.x / p.hkv;
+    attn_record(p, w)->parts = 0;
+  }
+  if (s.b < 0) return;
+  while (true) {
+    AttnItem it{};
+    it.b = s.b;
+    it.tile = s.tile;
+    it.row0 = s.row0;
+    it.fresh = s.fresh;
+    it.cached = s.cached;
+    const AttnTile t = attn_tile(p, it);
+    const int un = attn_units(p, s.fresh + s.cached);          // the tile's units: [first_unit, first_unit + un)
+    const long long first_unit = s.at - s.in_tile;
+    const int take = (int)min(s.end - s.at, (long long)(un - s.in_tile));
+    const int c_first = t.start + s.in_tile * p.step, c_end = min(t.end, c_first + take * p.step);
+    if (c_first < c_end) {                                     // a tile may end before its sequence's longest does
+      const long long last_unit = first_unit + (t.end - t.start + p.step - 1) / p.step - 1;
+      const int w0 = share_of(s.units, s.pieces, first_unit), w1 = share_of(s.units, s.pieces, last_unit);
+      // a share's first part goes to its slot 2 w, its last to 2 w + 1; those between are whole tiles
+      const int which = s.at == share_start(s.units, s.pieces, w) ? 0 : 1;
+      const int slot = w0 == w1 ? -1 : (2 * w + which) * p.hkv + h;
+      if (w == w0 + 1 && h == 0 && threadIdx.x == 0) {         // describes the tile for the join
+        const int first = 2 * w0 + (first_unit == share_start(s.units, s.pieces, w0) ? 0 : 1);
+        *attn_record(p, w) = AttnRecord{w1 - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv, 2 * w * p.hkv, 2 * p.hkv, 1};
+      }
+      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, h, c_first, c_end, slot, lds))
+        attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, c_first, c_end, slot, &lds);
+    }
+    s.at += take;
+    if (s.at >= s.end) return;
+    s.in_tile = 0;
+    if (++s.tile == attn_tiles(p, s.fresh, p.bm)) {            // on to the next sequence that has tiles
+      s.tile = 0;
+      do {
+        ++s.b;
+        s.row0 = (int)p.offs[s.b];
+        s.fresh = (int)p.offs[s.b + 1] - s.row0;
+      } while (s.fresh == 0);
+      s.cached = (int)p.cache_len[s.b];
+    }
+    __syncthreads();   // the next part's loads overwrite what the last one's join read
+  }
 }
 
-hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream) {
-#define QG_ATTN(DP, GRAN, NW)                                                                             \
-  do {                                                                                                    \
-    if (mt == 1) attention_rows_kernel<DP, GRAN, 1, NW><<<grid, NW * 64, 0, stream>>>(p);                 \
-    else attention_rows_kernel<DP, GRAN, 2, NW><<<grid, NW * 64, 0, stream>>>(p);                         \
+namespace {
+
+// f(kernel, waves per workgroup, LDS bytes) of the instance that serves a call.
+template <typename F>
+void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
+#define QG_ATTN(DP, GRAN, NW, NST)                                                                              \
+  do {                                                                                                          \
+    if (mt == 1) f(attention_rows_kernel<DP, GRAN, 1, NW, NST>, NW, sizeof(AttnRowsLds<DP, GRAN, 1, NW, NST>)); \
+    else f(attention_rows_kernel<DP, GRAN, 2, NW, NST>, NW, sizeof(AttnRowsLds<DP, GRAN, 2, NW, NST>));         \
   } while (0)
   const int gran = p.fp8 ? p.gran : 0;
   if (p.d <= 64) {
-    if (gran == 0) QG_ATTN(64, 0, 4);
-    else if (gran == 32) QG_ATTN(64, 32, 4);
-    else QG_ATTN(64, 64, 4);
+    if (gran == 0) QG_ATTN(64, 0, 4, 2);
+    else if (gran == 32) QG_ATTN(64, 32, 4, 2);
+    else QG_ATTN(64, 64, 4, 2);
   } else if (p.d <= 128) {
-    if (gran == 0) QG_ATTN(128, 0, 2);
-    else if (gran == 32) QG_ATTN(128, 32, 4);
-    else if (gran == 64) QG_ATTN(128, 64, 4);
-    else QG_ATTN(128, 128, 4);
+    if (gran == 0) QG_ATTN(128, 0, 2, 2);
+    else if (gran == 32) QG_ATTN(128, 32, 4, 2);
+    else if (gran == 64) QG_ATTN(128, 64, 4, 2);
+    else QG_ATTN(128, 128, 4, 2);
   } else {
-    if (gran == 0) QG_ATTN(256, 0, 2);
-    else if (gran == 32) QG_ATTN(256, 32, 2);
-    else if (gran == 64) QG_ATTN(256, 64, 2);
-    else QG_ATTN(256, 128, 2);
+    if (gran == 0) QG_ATTN(256, 0, 2, 2);
+    else if (gran == 32) QG_ATTN(256, 32, 2, 2);
+    else if (gran == 64) QG_ATTN(256, 64, 2, 2);
+    else QG_ATTN(256, 128, 2, 2);
   }
 #undef QG_ATTN
+}
+
+}  // namespace
+
+int attention_rows_resident(const AttnArgs& p, int mt) {
+  int n = 0;
+  // by LDS (160 KB per CU), and by registers: the kernels are built for two waves per SIMD
+  with_rows_kernel(p, mt, [&](auto, int nw, size_t lds) { n = p.num_cus * std::max(1, std::min((int)(163840 / lds), 8 / nw)); });
+  return n;
+}
+
+hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream) {
+  with_rows_kernel(p, mt, [&](auto kernel, int nw, size_t) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
   return hipGetLastError();
 }
 

@@ -93,6 +93,11 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   const int c_end = min(t.end, c_first + it.chunk);
   if (c_first >= c_end) return false;                               // the sequence's longer tiles need this chunk
   const bool alone = t.end - t.start <= it.chunk;
+  if (!SAFE && it.nsplit > 1 && it.split == 0 && h == 0 && threadIdx.x == 0) {   // one workgroup describes the tile for the join
+    const int first = (it.slots + it.tile * p.hkv * it.nsplit);
+    *attn_record(p, it.record) = AttnRecord{(t.end - t.start + it.chunk - 1) / it.chunk, it.row0, t.r_first, t.r_count,
+                                            first, first + 1, 1, it.nsplit};
+  }
 
   const int rows = it.fresh * p.group;
   int tok[RT], hi[RT], lo[RT];
@@ -449,7 +454,7 @@ template <int DP, int GRAN, int RT>
 __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
   __shared__ AttnTileLds<DP, GRAN> lds;
   const int h = blockIdx.x % p.hkv;
-  const AttnItem it = attn_locate<AW * 64>(p, lds.scan);
+  const AttnItem it = attn_locate<AW * 64>(p, blockIdx.x / p.hkv, h, lds.scan);
   if (it.b < 0) return;
   if (attend_tile<DP, GRAN, RT, false>(p, it, h, lds))
     attend_tile_safe<DP, GRAN, RT>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
