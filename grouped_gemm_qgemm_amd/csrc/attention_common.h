@@ -14,8 +14,8 @@
 // 2 * positions / chunk items, so all of them together have fewer than 2 * target.
 //
 // Shares (few rows): the positions of all tiles, in units of `step`, form one line
-// that is cut into `target / hkv` pieces of equal length, one per workgroup (and
-// head). A piece may hold the end of one tile, whole tiles, and the start of
+// that is cut into `target / (hkv / hw)` pieces of equal length, one per workgroup
+// (and group of hw heads), or fewer of at least `min_chunk` units. A piece may hold the end of one tile, whole tiles, and the start of
 // another, so every workgroup has the same amount to read, whatever the lengths.
 //
 // What a workgroup computes of a cut tile goes to the workspace, as does a record
@@ -32,7 +32,7 @@ typedef int i32x2v_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kAttnAlign = 64;   // a tile's first position is rounded down to this
+constexpr int kAttnAlign = 64;   // `step` at most (a power of two): a tile's first position is rounded down to it
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row's reference
 
 // What one workgroup works on.
@@ -215,11 +215,11 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem&
   t.t_last = (t.r_first + t.r_count - 1) / p.group;
   t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
   t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
-  t.start = t.begin / kAttnAlign * kAttnAlign;
+  t.start = t.begin & -p.step;   // so that the first unit, or chunk, holds a position that is seen
   return t;
 }
 
-// The share of workgroup w (of a head): units [at, end) of the line, of which `at` is
+// The share of workgroup w (of a group of heads): units [at, end) of the line, of which `at` is
 // unit `in_tile` of tile `tile` of sequence b. The line has `units` units in all and
 // `pieces` shares; b is -1 where the share is empty.
 struct AttnShare {
@@ -264,7 +264,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, int w, ShareS
   AttnShare s{};
 #pragma unroll
   for (int v = 0; v < NT / 64; ++v) s.units += sh.part[v];
-  s.pieces = (int)min((long long)max(p.target / p.hkv, 1), s.units);
+  s.pieces = (int)min((long long)max(p.target / (p.hkv / p.hw), 1), (s.units + p.min_chunk - 1) / p.min_chunk);
   if (w >= s.pieces) {
     s.b = -1;
     return s;
@@ -400,8 +400,9 @@ __device__ __forceinline__ Row16 rows_of16(const AttnArgs& p, page_list_t pages,
   return Row16{(size_t)pages[pg] * p.page_size + (x - pg * p.page_size), x};
 }
 
-// Shares per launch (over all heads) that run at once: `target` for launch_attention_rows.
-int attention_rows_resident(const AttnArgs& p, int mt);
+// Sets what launch_attention_rows goes by: `target`, the workgroups that run at once,
+// and `hw`, the heads per workgroup.
+void attention_rows_shape(AttnArgs& p, int mt);
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
 

@@ -18,7 +18,7 @@ namespace qg {
 namespace {
 
 constexpr int JT = 256;
-constexpr int kRowsMost = 1024, kRowsStep = 128;
+constexpr int kRowsMost = 512, kRowsStep = 32, kRowsUnits = 4, kRowsHeads = 4;
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -118,8 +118,9 @@ static hipError_t launch_join(const AttnArgs& p, long long cut, hipStream_t stre
 
 int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t hkv, int64_t d) {
   (void)T; (void)batch; (void)hq;
+  // two slots per share and head
   const int64_t rt = std::max<int64_t>(kRowsMost, hkv), tt = std::max<int64_t>(kTileTarget, hkv);
-  return std::max(attn_header_floats((int)rt) + 2 * rt * attn_slot_floats(32, dp_of(d)),
+  return std::max(attn_header_floats((int)rt) + 2 * kRowsHeads * rt * attn_slot_floats(32, dp_of(d)),
                   attn_header_floats((int)tt) + 2 * tt * attn_slot_floats(128, dp_of(d)));
 }
 
@@ -138,13 +139,17 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   const long long tiles = rows / p.bm + p.batch, room = p.max_pages * p.page_size;
   if (few) {
     p.step = kRowsStep;
-    p.target = std::max(std::min(attention_rows_resident(p, mt), kRowsMost), p.hkv);
-    const long long units = (room + p.step - 1) / p.step;
-    const long long shares = units < p.target ? std::min<long long>(p.target / p.hkv, tiles * units) : p.target / p.hkv;
-    const long long grid = (shares + 7) / 8 * 8 * p.hkv;
+    p.min_chunk = kRowsUnits;
+    attention_rows_shape(p, mt);
+    const int groups = p.hkv / p.hw;
+    p.target = std::max(std::min(p.target, kRowsMost), groups);
+    const long long units = (room + p.step - 1) / p.step;   // of a tile, at most
+    const long long shares = units < p.target ? std::min<long long>(p.target / groups, (tiles * units + p.min_chunk - 1) / p.min_chunk)
+                                              : p.target / groups;
+    const long long grid = (shares + 7) / 8 * 8 * groups;
     if (grid > INT32_MAX) return hipErrorNotSupported;
     const hipError_t e = launch_attention_rows(p, mt, (unsigned)grid, stream);
-    return e != hipSuccess || units <= 1 ? e : launch_join(p, shares, stream);   // one unit cannot be cut
+    return e != hipSuccess || shares <= 1 ? e : launch_join(p, shares, stream);   // one share has all its tiles whole
   }
   p.step = kTileStep;
   p.min_chunk = kTileMinChunk;

@@ -64,7 +64,7 @@ struct AttnRowsLds {
 // e4m3 cache, 0 for bf16. SAFE: values are selected per token. Without it, returns whether some output came out
 // as an infinity or NaN, for the whole workgroup, and then has written nothing.
 template <int DP, int GRAN, int MT, int NW, int NST, bool SAFE>
-__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h, int c_first, int c_end, int slot,
+__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h0, int hw, int c_first, int c_end, int slot,
                                             AttnRowsLds<DP, GRAN, MT, NW, NST>& lds) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int ES = FP8 ? 1 : 2;              // bytes per cached element
@@ -87,6 +87,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, j = lane >> 4;
+  const int h = h0 + wave % hw, phase = wave / hw, phases = NW / hw;   // this wave's head and blocks
   const AttnTile t = attn_tile(p, it);
 
   // rows of this lane, one per 16-row tile
@@ -218,15 +219,15 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 
     const int blocks = (s_end - s_first + 31) / 32;
     // NST - 1 blocks in flight besides the one in hand
-    const int my_blocks = wave < blocks ? (blocks - wave + NW - 1) / NW : 0;
+    const int my_blocks = phase < blocks ? (blocks - phase + phases - 1) / phases : 0;
 #pragma unroll
     for (int u = 0; u < NST - 1; ++u)
-      if (u < my_blocks) issue(wave + u * NW, u);
+      if (u < my_blocks) issue(phase + u * phases, u);
     int at = 0, to = NST - 1;
     for (int n = 0; n < my_blocks; ++n, at = at + 1 == NST ? 0 : at + 1) {
-      const int i = wave + n * NW;
+      const int i = phase + n * phases;
       if (n + NST - 1 < my_blocks) {
-        issue(i + (NST - 1) * NW, to);
+        issue(i + (NST - 1) * phases, to);
         to = to + 1 == NST ? 0 : to + 1;
       }
       wait_blocks<LB, NST - 1>(my_blocks - 1 - n);
@@ -418,17 +419,14 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n) *reinterpret_cast<float4_t*>(mine + (16 * mt + col) * OS + 16 * n + 4 * j) = acc[mt][n];
   }
   __syncthreads();
-  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)max(slot, 0) * attn_slot_floats(16 * MT, DP);
-  for (int e = tid; e < t.r_count * (DP / 4); e += NT) {
-    const int r = e / (DP / 4), d = e % (DP / 4) * 4;
+  for (int e = tid; e < hw * t.r_count * (DP / 4); e += NT) {
+    const int sub = e / (t.r_count * (DP / 4)), r = e / (DP / 4) % t.r_count, d = e % (DP / 4) * 4;
     float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) top = fmaxf(top, lds.w_m[w][r]);
+    for (int w = sub; w < NW; w += hw) top = fmaxf(top, lds.w_m[w][r]);
     const float base = top == -INFINITY ? 0.f : top;
     float4_t o = {0.f, 0.f, 0.f, 0.f};
     float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
+    for (int w = sub; w < NW; w += hw) {
       const float f = __builtin_amdgcn_exp2f(lds.w_m[w][r] - base);
       const float4_t x = *reinterpret_cast<const float4_t*>(reinterpret_cast<const float*>(&ring[w][0][0][0]) + r * OS + d);
 #pragma unroll
@@ -439,10 +437,11 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       if (d < p.d) {
         const int row = t.r_first + r;
         const float inv = 1.f / sum;   // every row sees a position
-        uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d + d;
+        uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + (h0 + sub) * p.group + row % p.group) * p.d + d;
         *reinterpret_cast<u32x2_t*>(to) = u32x2_t{f2bf2_rn(o[0] * inv, o[1] * inv), f2bf2_rn(o[2] * inv, o[3] * inv)};
       }
     } else {
+      float* ws = p.workspace + attn_header_floats(p.target) + (size_t)(slot + sub) * attn_slot_floats(16 * MT, DP);
       *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + d) = o;
       if (d == 0) {
         ws[16 * MT * DP + 2 * r] = top;
@@ -458,7 +457,7 @@ template <int DP, int GRAN, int MT, int NW, int NST>
 __device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int c_first, int c_end, int slot,
                                                            AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), blockIdx.x / 8 % p.hkv, __builtin_amdgcn_readfirstlane(c_first),
+  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), blockIdx.x / 8 % (p.hkv / p.hw) * p.hw, p.hw, __builtin_amdgcn_readfirstlane(c_first),
                                            __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds);
 }
 
@@ -467,10 +466,11 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
   __shared__ AttnRowsLds<DP, GRAN, MT, NW, NST> lds;
   // Workgroups go to the eight XCDs in turn: all heads of a share to one of them, so
   // that its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
-  const int h = blockIdx.x / 8 % p.hkv, w = blockIdx.x / 8 / p.hkv * 8 + blockIdx.x % 8;
+  const int groups = p.hkv / p.hw;
+  const int h = blockIdx.x / 8 % groups * p.hw, w = blockIdx.x / 8 / groups * 8 + blockIdx.x % 8;
   AttnShare s = attn_share<NW * 64>(p, w, lds.scan);
   if (h == 0 && threadIdx.x == 0) {
-    if (w == 0) *attn_record_count(p) = gridDim.x / p.hkv;
+    if (w == 0) *attn_record_count(p) = gridDim.x / groups;
     attn_record(p, w)->parts = 0;
   }
   if (s.b < 0) return;
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
         const int first = 2 * w0 + (first_unit == share_start(s.units, s.pieces, w0) ? 0 : 1);
         *attn_record(p, w) = AttnRecord{w1 - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv, 2 * w * p.hkv, 2 * p.hkv, 1};
       }
-      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, h, c_first, c_end, slot, lds))
+      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, h, p.hw, c_first, c_end, slot, lds))
         attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, c_first, c_end, slot, &lds);
     }
     s.at += take;
@@ -531,7 +531,7 @@ void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
     else if (gran == 32) QG_ATTN(64, 32, 4, 2);
     else QG_ATTN(64, 64, 4, 2);
   } else if (p.d <= 128) {
-    if (gran == 0) QG_ATTN(128, 0, 2, 2);
+    if (gran == 0) QG_ATTN(128, 0, 4, 2);
     else if (gran == 32) QG_ATTN(128, 32, 4, 2);
     else if (gran == 64) QG_ATTN(128, 64, 4, 2);
     else QG_ATTN(128, 128, 4, 2);
@@ -546,11 +546,14 @@ void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
 
 }  // namespace
 
-int attention_rows_resident(const AttnArgs& p, int mt) {
-  int n = 0;
-  // by LDS (160 KB per CU), and by registers: the kernels are built for two waves per SIMD
-  with_rows_kernel(p, mt, [&](auto, int nw, size_t lds) { n = p.num_cus * std::max(1, std::min((int)(163840 / lds), 8 / nw)); });
-  return n;
+void attention_rows_shape(AttnArgs& p, int mt) {
+  with_rows_kernel(p, mt, [&](auto, int nw, size_t lds) {
+    // resident workgroups: by LDS (160 KB per CU), and by registers (the kernels are built
+    // for two waves per SIMD)
+    p.target = p.num_cus * std::max(1, std::min((int)(163840 / lds), 8 / nw));
+    p.hw = nw;
+    while (p.hkv % p.hw != 0) p.hw /= 2;
+  });
 }
 
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream) {

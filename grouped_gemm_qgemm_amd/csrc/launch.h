@@ -121,7 +121,7 @@ struct AttnArgs {
   float scale;
   // the launcher's: page_size as a multiplication, and how the work is cut (attention_common.h)
   uint32_t div_mul = 0, div_shift = 0;
-  int bm = 0, target = 0, min_chunk = 0, step = 0;
+  int bm = 0, target = 0, min_chunk = 0, step = 0, hw = 1;
 };
 
 // Decode-shaped W4A16 (M <= 16).

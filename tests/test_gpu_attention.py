@@ -409,3 +409,15 @@ def test_a_serving_run(lib, gpu, gran):
                                   layer_idx=0, scales=now_s, gran=gran)
         compare(d, host16(out), exact(d, hd ** -0.5), f"step {step}")
         cached_h = cached_h + np.array(new, np.uint32)
+
+
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("history", [1531, 1563, 1595])
+def test_a_window_that_starts_anywhere_in_a_block(lib, gpu, page, history):
+    """The first position seen, and the parts that the work is cut into, at every place of 32 and
+    64: no part may consist of positions (and pages) before it."""
+    d = synth.attention_inputs(35, [1, 2, 1], [history, history + 7, history + 20], hq=4, hkv=1, d=64, page=page, layers=1)
+    ref = exact(d, 0.125, True, 1500)
+    for b in range(3):
+        d.page_table[b, :(int(d.cache_lengths[b]) - 1499) // page] = 0xFFFFFFFF
+    compare(d, run(lib, d, 0.125, True, 1500), ref)
