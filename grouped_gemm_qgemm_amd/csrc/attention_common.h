@@ -109,16 +109,16 @@ __device__ __forceinline__ AttnRecord* attn_record(const AttnArgs& p, int i) {
   return reinterpret_cast<AttnRecord*>(p.workspace + (size_t)kRecordInts * (i + 1));
 }
 
-// Tiles of a sequence, and the positions its longest tile may cover.
-__device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh, int bm) {
-  return (fresh * p.group + bm - 1) / bm;
+// x / d for the divisor that (mul, shift) were made for; x < 2^31
+__device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t mul, uint32_t shift) {
+  return (__umulhi(x, mul) + x) >> shift;
 }
-__device__ __forceinline__ int attn_span(const AttnArgs& p, int len, int bm) {
-  if (!p.window) return len;
-  // a tile of bm rows has tokens t .. t + (bm - 1) / group + 1 at most
-  const long long w = (long long)p.window + (bm - 1) / p.group + 1 + kAttnAlign;
-  return (int)(w < len ? w : (long long)len);
-}
+__device__ __forceinline__ int over_group(const AttnArgs& p, int x) { return (int)fast_div(x, p.group_mul, p.group_shift); }
+
+// Tiles of a sequence, and the positions its longest tile may cover (window_span: the
+// window and what a tile's tokens and the rounding of its start add to it).
+__device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh) { return (fresh * p.group + p.bm - 1) >> p.bm_log2; }
+__device__ __forceinline__ int attn_span(const AttnArgs& p, int len) { return p.window ? min(len, p.window_span) : len; }
 
 template <int NT>
 struct AttnScan {
@@ -141,7 +141,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
       if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
-      cost += (unsigned long long)attn_tiles(p, fresh, p.bm) * (unsigned)attn_span(p, len, p.bm);
+      cost += (unsigned long long)attn_tiles(p, fresh) * (unsigned)attn_span(p, len);
     }
   }
 #pragma unroll
@@ -154,7 +154,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
   for (int w = 0; w < NT / 64; ++w) cost += sh.cost[w];
   const unsigned long long even = (cost * (unsigned)p.hkv + p.target - 1) / (unsigned)p.target;
   int chunk = even < (unsigned long long)p.min_chunk ? p.min_chunk : even > INT32_MAX / 2 ? INT32_MAX / 2 : (int)even;
-  chunk = (chunk + p.step - 1) / p.step * p.step;
+  chunk = (chunk + p.step - 1) & -p.step;
 
   int base = 0, slot_base = 0, cut_base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
@@ -166,8 +166,8 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
         fresh = (int)p.offs[b + 1] - row0;
         len = fresh + (int)p.cache_len[b];
       }
-      tiles = attn_tiles(p, fresh, p.bm);
-      if (tiles) ns = (attn_span(p, len, p.bm) + chunk - 1) / chunk;
+      tiles = attn_tiles(p, fresh);
+      if (tiles) ns = (attn_span(p, len) + chunk - 1) / chunk;
     }
     const int items = tiles * ns, cuts = ns > 1 ? tiles : 0, slots = cuts * ns * p.hkv;
     int ii = items, is = slots, ic = cuts;
@@ -209,97 +209,87 @@ struct AttnTile {
 
 __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem& it) {
   AttnTile t;
-  t.r_first = it.tile * p.bm;
+  t.r_first = it.tile << p.bm_log2;
   t.r_count = min(it.fresh * p.group - t.r_first, p.bm);
-  t.t_first = t.r_first / p.group;
-  t.t_last = (t.r_first + t.r_count - 1) / p.group;
+  t.t_first = over_group(p, t.r_first);
+  t.t_last = over_group(p, t.r_first + t.r_count - 1);
   t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
   t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
   t.start = t.begin & -p.step;   // so that the first unit, or chunk, holds a position that is seen
   return t;
 }
 
-// The share of workgroup w (of a group of heads): units [at, end) of the line, of which `at` is
-// unit `in_tile` of tile `tile` of sequence b. The line has `units` units in all and
-// `pieces` shares; b is -1 where the share is empty.
+// The line's cut into `pieces` shares: the first `extra` have one unit more than `each`.
+struct AttnCut {
+  uint32_t units, pieces, each, extra;
+  __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * each + min(w, extra); }
+  // the share that holds unit u
+  __device__ __forceinline__ uint32_t of(uint32_t u) const {
+    const uint32_t big = extra * (each + 1);
+    return u < big ? u / (each + 1) : extra + (u - big) / each;
+  }
+};
+// The share of workgroup w (of a group of heads): units [at, end) of the line, of which
+// `at` is unit `in_tile` of tile `tile` of sequence b; b is -1 where there is no share.
 struct AttnShare {
-  long long units, at, end;
-  int pieces, b, tile, in_tile;
+  AttnCut cut;
+  uint32_t at, end;
+  int b, tile, in_tile;
   int row0, fresh, cached;    // of sequence b
 };
-__device__ __forceinline__ long long share_start(long long units, int pieces, int w) { return units * w / pieces; }
-// the workgroup whose share holds unit u
-__device__ __forceinline__ int share_of(long long units, int pieces, long long u) {
-  return (int)(((u + 1) * pieces + units - 1) / units) - 1;
-}
 // units of each tile of a sequence
-__device__ __forceinline__ int attn_units(const AttnArgs& p, int len) { return (attn_span(p, len, p.bm) + p.step - 1) / p.step; }
+__device__ __forceinline__ int attn_units(const AttnArgs& p, int len) { return (attn_span(p, len) + p.step - 1) >> p.step_log2; }
 
 template <int NT>
 struct ShareScan {
-  long long part[NT / 64];
+  uint32_t part[NT / 64];
   AttnShare found;
 };
 
 template <int NT>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, int w, ShareScan<NT>& sh) {
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, uint32_t w, ShareScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  long long mine = 0;
+  // a thread's sequences; of up to NT, the prefix sum over them is the total as well
+  uint32_t units0 = 0, all = 0;
   int row00 = 0, fresh0 = 0, len0 = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
     const int b = b0 + tid;
     if (b < p.batch) {
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
-      if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
-      mine += (long long)attn_tiles(p, fresh, p.bm) * attn_units(p, len);
+      const uint32_t units = (uint32_t)(attn_tiles(p, fresh) * attn_units(p, len));
+      if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; units0 = units; }
+      all += units;
     }
   }
-  const long long first_mine = mine;   // of sequence tid, where the batch has at most NT
+  uint32_t incl = all;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) mine += __shfl_xor(mine, d);
-  if (lane == 0) sh.part[wave] = mine;
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t v = __shfl_up(incl, d);
+    if (lane >= d) incl += v;
+  }
+  if (lane == 63) sh.part[wave] = incl;
   if (tid == 0) sh.found.b = -1;
   __syncthreads();
   AttnShare s{};
+  uint32_t before = 0;
 #pragma unroll
-  for (int v = 0; v < NT / 64; ++v) s.units += sh.part[v];
-  s.pieces = (int)min((long long)max(p.target / (p.hkv / p.hw), 1), (s.units + p.min_chunk - 1) / p.min_chunk);
-  if (w >= s.pieces) {
+  for (int v = 0; v < NT / 64; ++v) {
+    if (v < wave) before += sh.part[v];
+    s.cut.units += sh.part[v];
+  }
+  s.cut.pieces = min((uint32_t)max(p.target / (p.hkv / p.hw), 1), (s.cut.units + p.min_chunk - 1) / p.min_chunk);
+  if (w >= s.cut.pieces) {
     s.b = -1;
     return s;
   }
-  s.at = share_start(s.units, s.pieces, w);
-  s.end = share_start(s.units, s.pieces, w + 1);
-  long long base = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += NT) {
-    const int b = b0 + tid;
-    int row0 = row00, fresh = fresh0, len = len0;
-    long long units = b0 == 0 && p.batch <= NT ? first_mine : 0;
-    if (p.batch > NT && b < p.batch) {
-      row0 = (int)p.offs[b];
-      fresh = (int)p.offs[b + 1] - row0;
-      len = fresh + (int)p.cache_len[b];
-      units = (long long)attn_tiles(p, fresh, p.bm) * attn_units(p, len);
-    }
-    long long incl = units;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const long long v = __shfl_up(incl, d);
-      if (lane >= d) incl += v;
-    }
-    __syncthreads();
-    if (lane == 63) sh.part[wave] = incl;
-    __syncthreads();
-    long long before = base;
-#pragma unroll
-    for (int v = 0; v < NT / 64; ++v) {
-      if (v < wave) before += sh.part[v];
-      base += sh.part[v];
-    }
-    const long long first = before + incl - units;
-    if (s.at >= first && s.at < before + incl) {
-      const int un = attn_units(p, len), local = (int)(s.at - first);
+  s.cut.each = s.cut.units / s.cut.pieces;
+  s.cut.extra = s.cut.units % s.cut.pieces;
+  s.at = s.cut.start(w);
+  s.end = s.cut.start(w + 1);
+  auto look = [&](int b, uint32_t first, uint32_t units, int row0, int fresh, int len) {
+    if (s.at >= first && s.at - first < units) {
+      const uint32_t un = attn_units(p, len), local = s.at - first;
       sh.found.b = b;
       sh.found.tile = local / un;
       sh.found.in_tile = local % un;
@@ -307,8 +297,41 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, int w, ShareS
       sh.found.fresh = fresh;
       sh.found.cached = len - fresh;
     }
+  };
+  if (p.batch <= NT) {
+    look(tid, before + incl - all, units0, row00, fresh0, len0);
     __syncthreads();
-    if (s.at < base) break;
+  } else {
+    uint32_t base = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += NT) {
+      const int b = b0 + tid;
+      int row0 = 0, fresh = 0, len = 0;
+      uint32_t units = 0;
+      if (b < p.batch) {
+        row0 = (int)p.offs[b];
+        fresh = (int)p.offs[b + 1] - row0;
+        len = fresh + (int)p.cache_len[b];
+        units = (uint32_t)(attn_tiles(p, fresh) * attn_units(p, len));
+      }
+      uint32_t run = units;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t v = __shfl_up(run, d);
+        if (lane >= d) run += v;
+      }
+      __syncthreads();
+      if (lane == 63) sh.part[wave] = run;
+      __syncthreads();
+      uint32_t first = base + run - units;
+#pragma unroll
+      for (int v = 0; v < NT / 64; ++v) {
+        if (v < wave) first += sh.part[v];
+        base += sh.part[v];
+      }
+      look(b, first, units, row0, fresh, len);
+      __syncthreads();
+      if (s.at < base) break;
+    }
   }
   s.b = __builtin_amdgcn_readfirstlane(sh.found.b);
   s.tile = __builtin_amdgcn_readfirstlane(sh.found.tile);
@@ -316,12 +339,13 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, int w, ShareS
   s.row0 = __builtin_amdgcn_readfirstlane(sh.found.row0);
   s.fresh = __builtin_amdgcn_readfirstlane(sh.found.fresh);
   s.cached = __builtin_amdgcn_readfirstlane(sh.found.cached);
+  s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
+  s.cut.pieces = __builtin_amdgcn_readfirstlane(s.cut.pieces);
+  s.cut.each = __builtin_amdgcn_readfirstlane(s.cut.each);
+  s.cut.extra = __builtin_amdgcn_readfirstlane(s.cut.extra);
+  s.at = s.cut.start(w);
+  s.end = s.cut.start(w + 1);
   return s;
-}
-
-// x / d for the divisor that (mul, shift) were made for; x < 2^31
-__device__ __forceinline__ uint32_t fast_div(uint32_t x, uint32_t mul, uint32_t shift) {
-  return (__umulhi(x, mul) + x) >> shift;
 }
 
 // four e4m3 codes -> four bf16 (exact)

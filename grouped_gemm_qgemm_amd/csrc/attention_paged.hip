@@ -10,6 +10,7 @@
 // part to finish: that needs counters which every call must find at zero, and
 // ordering between the XCDs' caches within a kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention_common.h"
 
@@ -18,101 +19,90 @@ namespace qg {
 namespace {
 
 constexpr int JT = 256;
-constexpr int kRowsMost = 512, kRowsStep = 32, kRowsUnits = 4, kRowsHeads = 4;
+constexpr int kRowsMost = 512, kRowsStep = 32, kRowsUnits = 1, kRowsHeads = 4;
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
 }  // namespace
 
-// WPR waves share a row's parts (4 where rows are few, 1 else).
-template <int DP, int WPR>
+// A wave per row: its lanes take DP / 4 groups of four floats of 256 / DP parts at a
+// time, eight such steps in flight, so that a row of up to 2048 / DP parts costs one
+// memory latency after its record's.
+template <int DP>
 __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int parts, int rows_per_wg) {
-  constexpr int VL = DP / 64;   // floats per lane
-  __shared__ float part[WPR > 1 ? 4 : 1][DP + 1];
+  constexpr int LR = DP / 4, PH = 64 / LR;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = blockIdx.x % p.hkv, at = blockIdx.x / p.hkv;
-  if (at / parts >= *attn_record_count(p)) return;
   const AttnRecord t = *attn_record(p, at / parts);
+  if (at / parts >= *attn_record_count(p) || t.parts <= 1) return;   // (or written by the one that computed it)
   const int ns = t.parts;
-  if (ns <= 1) return;   // written by the one that computed it
   const long long slot_floats = attn_slot_floats(p.bm, DP);
   const float* slots = p.workspace + attn_header_floats(p.target);
   auto part_at = [&](int s) {
     return slots + (long long)((s == 0 ? t.first : t.next + (s - 1) * t.step) + h * t.head_step) * slot_floats;
   };
+  const int d = lane % LR * 4, phase = lane / LR;
   const int r0 = at % parts * rows_per_wg, r1 = min(t.r_count, r0 + rows_per_wg);
-  for (int r = r0 + (WPR > 1 ? 0 : wave); r < r1; r += WPR > 1 ? 1 : 4) {
+  for (int r = r0 + wave; r < r1; r += JT / 64) {
     const int ml = p.bm * DP + 2 * r;   // a row's maximum and sum in a slot
     float top = -INFINITY;
     for (int s = lane; s < ns; s += 64) top = fmaxf(top, part_at(s)[ml]);
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int k = 32; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
     const float base = top == -INFINITY ? 0.f : top;
-    float o[VL], sum = 0.f;
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
+    float sum = 0.f;
+    auto add = [&](auto steps, int s0) {   // parts s0, s0 + PH, ..: `steps` of them
+      constexpr int U = decltype(steps)::value;
+      float4_t x[U];
+      float2_t m[U];
 #pragma unroll
-    for (int i = 0; i < VL; ++i) o[i] = 0.f;
-    for (int s0 = 0; s0 < ns; s0 += 64) {
-      float f = 0.f;
-      if (s0 + lane < ns) {
-        const float* x = part_at(s0 + lane) + ml;
-        f = __builtin_amdgcn_exp2f(x[0] - base);
-        sum = __builtin_fmaf(x[1], f, sum);
+      for (int u = 0; u < U; ++u) {
+        const float* from = part_at(min(s0 + u * PH, ns - 1));
+        x[u] = *reinterpret_cast<const float4_t*>(from + (size_t)r * DP + d);
+        m[u] = *reinterpret_cast<const float2_t*>(from + ml);
       }
-      const int n = min(64, ns - s0);
-      for (int s = WPR > 1 ? wave : 0; s < n; s += 8 * WPR) {   // eight parts' loads in flight
-        float x[8][VL], fs[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int su = s + u * WPR;
-          fs[u] = su < n ? __shfl(f, su) : 0.f;
-          const float* at_u = part_at(s0 + min(su, n - 1)) + r * DP + lane * VL;
+      for (int u = 0; u < U; ++u) {
+        const float f = __builtin_amdgcn_exp2f(m[u].x - base);
+        if (s0 + u * PH < ns) {
+          sum = __builtin_fmaf(m[u].y, f, sum);
 #pragma unroll
-          for (int i = 0; i < VL; ++i) x[u][i] = at_u[i];
+          for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i], f, o[i]);
         }
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-#pragma unroll
-          for (int i = 0; i < VL; ++i) o[i] = __builtin_fmaf(x[u][i], fs[u], o[i]);
       }
+    };
+    if (ns <= 2 * PH) {
+      add(std::integral_constant<int, 2>{}, phase);
+    } else {
+      for (int s0 = phase; s0 < ns; s0 += 8 * PH) add(std::integral_constant<int, 8>{}, s0);
     }
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);   // every wave has all parts' sums
-    if constexpr (WPR > 1) {
-      __syncthreads();
+    for (int k = LR; k < 64; k <<= 1) {
+      sum += __shfl_xor(sum, k);
 #pragma unroll
-      for (int i = 0; i < VL; ++i) part[wave][lane * VL + i] = o[i];
-      __syncthreads();
-      if (wave != 0) continue;
-#pragma unroll
-      for (int i = 0; i < VL; ++i) o[i] = (part[0][lane * VL + i] + part[1][lane * VL + i]) + (part[2][lane * VL + i] + part[3][lane * VL + i]);
+      for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], k);
     }
     const float inv = 1.f / sum;
-    const int row = t.r_first + r;
-    uint16_t* to = p.out + ((size_t)(t.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
-#pragma unroll
-    for (int i = 0; i < VL; ++i)
-      if (lane * VL + i < p.d) to[lane * VL + i] = (uint16_t)f2bf2_rn(o[i] * inv, 0.f);
+    const int row = t.r_first + r, token = over_group(p, row);
+    uint16_t* to = p.out + ((size_t)(t.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
+    if (phase == 0 && d < p.d)
+      *reinterpret_cast<u32x2_t*>(to + d) = u32x2_t{f2bf2_rn(o[0] * inv, o[1] * inv), f2bf2_rn(o[2] * inv, o[3] * inv)};
   }
 }
 
 // cut: records, at most
 static hipError_t launch_join(const AttnArgs& p, long long cut, hipStream_t stream) {
   const long long rows = std::min<long long>(p.bm, p.T * p.group);
-  const bool few = cut * p.hkv * rows <= 8 * p.num_cus;
-  const int per_wg = few ? 1 : 16;
+  // a row per wave where that still is about one round of workgroups
+  const int per_wg = cut * p.hkv * rows <= 64LL * p.num_cus ? 4 : 16;
   const long long parts = (rows + per_wg - 1) / per_wg;
   const dim3 grid((unsigned)(cut * parts * p.hkv));
-#define QG_JOIN(DP)                                                                                 \
-  do {                                                                                              \
-    if (few) attention_join_kernel<DP, 4><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);          \
-    else attention_join_kernel<DP, 1><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);              \
-  } while (0)
-  if (p.d <= 64) QG_JOIN(64);
-  else if (p.d <= 128) QG_JOIN(128);
-  else QG_JOIN(256);
-#undef QG_JOIN
+  if (p.d <= 64) attention_join_kernel<64><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
+  else if (p.d <= 128) attention_join_kernel<128><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
+  else attention_join_kernel<256><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
   return hipGetLastError();
 }
 
@@ -124,21 +114,40 @@ int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t 
                   attn_header_floats((int)tt) + 2 * tt * attn_slot_floats(128, dp_of(d)));
 }
 
+static int log2_of(int x) {
+  int k = 0;
+  while ((1 << k) < x) ++k;
+  return k;
+}
+
+// x / d for x < 2^31 as (umulhi(x, mul) + x) >> shift
+static void divide_by(int d, uint32_t& mul, uint32_t& shift) {
+  shift = log2_of(d);
+  mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)d)) / (uint64_t)d) + 1);
+}
+
+// Sets how the work is cut: rows per tile, positions per unit.
+static void set_shape(AttnArgs& p, int bm, int step) {
+  p.bm = bm;
+  p.bm_log2 = log2_of(bm);
+  p.step = step;
+  p.step_log2 = log2_of(step);
+  // a tile has tokens t .. t + (bm - 1) / group + 1 at most
+  const long long span = (long long)p.window + (bm - 1) / p.group + 1 + kAttnAlign;
+  p.window_span = (int)std::min<long long>(span, INT32_MAX);
+}
+
 hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   AttnArgs p = args;
-  // x / page_size for x < 2^31: (umulhi(x, mul) + x) >> shift
-  int shift = 0;
-  while ((1u << shift) < (uint32_t)p.page_size) ++shift;
-  p.div_shift = shift;
-  p.div_mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)p.page_size)) / (uint64_t)p.page_size) + 1);
+  divide_by(p.page_size, p.div_mul, p.div_shift);
+  divide_by(p.group, p.group_mul, p.group_shift);
   const long long rows = p.T * p.group;
   const bool few = rows <= 32LL * p.batch;
   const int mt = rows > 16LL * p.batch ? 2 : 1;
-  p.bm = few ? 16 * mt : 128;
+  set_shape(p, few ? 16 * mt : 128, few ? kRowsStep : kTileStep);
   // sequence b has ceil(new_b * group / bm) tiles per key/value head, of at most `room` positions
   const long long tiles = rows / p.bm + p.batch, room = p.max_pages * p.page_size;
   if (few) {
-    p.step = kRowsStep;
     p.min_chunk = kRowsUnits;
     attention_rows_shape(p, mt);
     const int groups = p.hkv / p.hw;
@@ -147,11 +156,10 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const long long shares = units < p.target ? std::min<long long>(p.target / groups, (tiles * units + p.min_chunk - 1) / p.min_chunk)
                                               : p.target / groups;
     const long long grid = (shares + 7) / 8 * 8 * groups;
-    if (grid > INT32_MAX) return hipErrorNotSupported;
+    if (grid > INT32_MAX || units > INT32_MAX / tiles) return hipErrorNotSupported;   // units are counted in 32 bits
     const hipError_t e = launch_attention_rows(p, mt, (unsigned)grid, stream);
     return e != hipSuccess || shares <= 1 ? e : launch_join(p, shares, stream);   // one share has all its tiles whole
   }
-  p.step = kTileStep;
   p.min_chunk = kTileMinChunk;
   p.target = std::max(kTileTarget, p.hkv);
   // Items: at most target / hkv + tiles (a chunk is at least the work over the target),

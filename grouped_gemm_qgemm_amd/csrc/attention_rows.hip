@@ -54,6 +54,7 @@ struct AttnRowsLds {
   __attribute__((aligned(16))) float ring_s[GRAN > 0 ? NW : 1][NST][R][2][32];   // run scales [run][keys, values][position]
   uint32_t pages[RPG];
   float w_m[NW][16 * MT], w_l[NW][16 * MT];
+  int w_off[NW];
   ShareScan<NW * 64> scan;
 };
 
@@ -97,10 +98,10 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = min(t.r_first + 16 * mt + col, rows - 1);
-    tok[mt] = r / p.group;
+    tok[mt] = over_group(p, r);
     hi[mt] = p.causal ? it.cached + tok[mt] : it.cached + it.fresh - 1;
     lo[mt] = p.window ? it.cached + tok[mt] - p.window + 1 : 0;
-    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[mt]) * p.hq + h * p.group + r % p.group) * p.d;
+    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[mt]) * p.hq + h * p.group + r - tok[mt] * p.group) * p.d;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int d = 32 * s + 8 * j;
@@ -131,10 +132,6 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     voff[k] = (key & 15) * row_bytes + c * 16;
     there[k] = c < chunks;
   }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int s = 0; s < NS; ++s) arrived(qf[mt][s]);
 
   float4_t acc[MT][ND];
   float m[MT], l[MT];     // reference of the weights' exponents (base 2), this lane's share of their sum
@@ -223,6 +220,10 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 #pragma unroll
     for (int u = 0; u < NST - 1; ++u)
       if (u < my_blocks) issue(phase + u * phases, u);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) arrived(qf[mt][s]);   // (with the first blocks, which are waited for next anyway)
     int at = 0, to = NST - 1;
     for (int n = 0; n < my_blocks; ++n, at = at + 1 == NST ? 0 : at + 1) {
       const int i = phase + n * phases;
@@ -393,19 +394,19 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       }
     }
   }
+  int off = 0;
   if (!SAFE) {
-    int off = 0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int n = 0; n < ND; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) off |= !(fabsf(acc[mt][n][i]) < INFINITY);
-    if (__syncthreads_or(off)) return true;
+    off = __any(off);
+    if (lane == 0) lds.w_off[wave] = off;
   }
 
   // the waves' results joined through LDS (their rings, which no load targets any more)
-  __syncthreads();
   float* mine = reinterpret_cast<float*>(&ring[wave][0][0][0]);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -419,6 +420,15 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n) *reinterpret_cast<float4_t*>(mine + (16 * mt + col) * OS + 16 * n + 4 * j) = acc[mt][n];
   }
   __syncthreads();
+  if (!SAFE) {
+    off = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) off |= lds.w_off[w];
+    if (off) {
+      __syncthreads();   // before the rings are used again
+      return true;
+    }
+  }
   for (int e = tid; e < hw * t.r_count * (DP / 4); e += NT) {
     const int sub = e / (t.r_count * (DP / 4)), r = e / (DP / 4) % t.r_count, d = e % (DP / 4) * 4;
     float top = -INFINITY;
@@ -435,9 +445,9 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     }
     if (slot < 0) {
       if (d < p.d) {
-        const int row = t.r_first + r;
+        const int row = t.r_first + r, token = over_group(p, row);
         const float inv = 1.f / sum;   // every row sees a position
-        uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + (h0 + sub) * p.group + row % p.group) * p.d + d;
+        uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + (h0 + sub) * p.group + row - token * p.group) * p.d + d;
         *reinterpret_cast<u32x2_t*>(to) = u32x2_t{f2bf2_rn(o[0] * inv, o[1] * inv), f2bf2_rn(o[2] * inv, o[3] * inv)};
       }
     } else {
@@ -483,18 +493,20 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
     it.cached = s.cached;
     const AttnTile t = attn_tile(p, it);
     const int un = attn_units(p, s.fresh + s.cached);          // the tile's units: [first_unit, first_unit + un)
-    const long long first_unit = s.at - s.in_tile;
-    const int take = (int)min(s.end - s.at, (long long)(un - s.in_tile));
+    const uint32_t first_unit = s.at - s.in_tile;
+    const int take = min((int)(s.end - s.at), un - s.in_tile);
     const int c_first = t.start + s.in_tile * p.step, c_end = min(t.end, c_first + take * p.step);
     if (c_first < c_end) {                                     // a tile may end before its sequence's longest does
-      const long long last_unit = first_unit + (t.end - t.start + p.step - 1) / p.step - 1;
-      const int w0 = share_of(s.units, s.pieces, first_unit), w1 = share_of(s.units, s.pieces, last_unit);
+      const uint32_t last_unit = first_unit + ((t.end - t.start + p.step - 1) >> p.step_log2) - 1;
+      const uint32_t begin = s.cut.start(w);
       // a share's first part goes to its slot 2 w, its last to 2 w + 1; those between are whole tiles
-      const int which = s.at == share_start(s.units, s.pieces, w) ? 0 : 1;
-      const int slot = w0 == w1 ? -1 : (2 * w + which) * p.hkv + h;
-      if (w == w0 + 1 && h == 0 && threadIdx.x == 0) {         // describes the tile for the join
-        const int first = 2 * w0 + (first_unit == share_start(s.units, s.pieces, w0) ? 0 : 1);
-        *attn_record(p, w) = AttnRecord{w1 - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv, 2 * w * p.hkv, 2 * p.hkv, 1};
+      const int slot = first_unit >= begin && last_unit < s.end ? -1 : (2 * w + (s.at == begin ? 0 : 1)) * p.hkv + h;
+      if (first_unit < begin && h == 0 && threadIdx.x == 0) {
+        const int w0 = s.cut.of(first_unit);
+        if (w == w0 + 1) {                                     // the tile's second share describes it for the join
+          const int first = 2 * w0 + (first_unit == s.cut.start(w0) ? 0 : 1);
+          *attn_record(p, w) = AttnRecord{(int)s.cut.of(last_unit) - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv, 2 * w * p.hkv, 2 * p.hkv, 1};
+        }
       }
       if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, h, p.hw, c_first, c_end, slot, lds))
         attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, c_first, c_end, slot, &lds);
@@ -502,7 +514,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
     s.at += take;
     if (s.at >= s.end) return;
     s.in_tile = 0;
-    if (++s.tile == attn_tiles(p, s.fresh, p.bm)) {            // on to the next sequence that has tiles
+    if (++s.tile == attn_tiles(p, s.fresh)) {            // on to the next sequence that has tiles
       s.tile = 0;
       do {
         ++s.b;

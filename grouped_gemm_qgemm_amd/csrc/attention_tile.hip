@@ -60,6 +60,7 @@ struct AttnTileLds {
   __attribute__((aligned(16))) u32x4_t ring[2][2][KB * DP / 8];                                   // [block parity][keys, values]
   __attribute__((aligned(16))) float ring_s[GRAN > 0 ? 2 : 1][2][R][GRAN > 0 ? KB : 1];   // [keys, values][run][position]
   uint32_t pages[TPG];
+  int w_off[AW];
   AttnScan<AW * 64> scan;
 };
 
@@ -105,10 +106,10 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int r = min(t.r_first + (wave * RT + rt) * 32 + col, rows - 1);
-    tok[rt] = r / p.group;
+    tok[rt] = over_group(p, r);
     hi[rt] = p.causal ? it.cached + tok[rt] : it.cached + it.fresh - 1;
     lo[rt] = p.window ? it.cached + tok[rt] - p.window + 1 : 0;
-    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[rt]) * p.hq + h * p.group + r % p.group) * p.d;
+    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[rt]) * p.hq + h * p.group + r - tok[rt] * p.group) * p.d;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const int d = 16 * s + 8 * half;
@@ -404,7 +405,15 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
       for (int n = 0; n < ND; ++n)
 #pragma unroll
         for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[rt][n][e]) < INFINITY);
-    if (!SAFE && __syncthreads_or(off)) return true;
+    if (!SAFE) {
+      off = __any(off);
+      if (lane == 0) lds.w_off[wave] = off;
+      __syncthreads();
+      off = 0;
+#pragma unroll
+      for (int w = 0; w < AW; ++w) off |= lds.w_off[w];
+      if (off) return true;
+    }
   }
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
@@ -416,8 +425,8 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     if (r >= t.r_count) continue;
     if (alone) {
       const float inv = 1.f / sum;   // every row sees a position
-      const int row = t.r_first + r;
-      uint16_t* to = p.out + ((size_t)(it.row0 + row / p.group) * p.hq + h * p.group + row % p.group) * p.d;
+      const int row = t.r_first + r, token = over_group(p, row);
+      uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
 #pragma unroll
       for (int n = 0; n < ND; ++n)
 #pragma unroll

@@ -119,9 +119,11 @@ struct AttnArgs {
   int64_t T, max_pages, pages;
   int batch, hq, hkv, group, d, page_size, layer, gran, causal, window, fp8, num_cus;
   float scale;
-  // the launcher's: page_size as a multiplication, and how the work is cut (attention_common.h)
-  uint32_t div_mul = 0, div_shift = 0;
-  int bm = 0, target = 0, min_chunk = 0, step = 0, hw = 1;
+  // the launcher's: page_size and group as multiplications, and how the work is cut
+  // (attention_common.h); bm and step are powers of two
+  uint32_t div_mul = 0, div_shift = 0, group_mul = 0, group_shift = 0;
+  int bm = 0, bm_log2 = 0, step = 0, step_log2 = 0, window_span = 0;
+  int target = 0, min_chunk = 0, hw = 1;
 };
 
 // Decode-shaped W4A16 (M <= 16).
