@@ -14,8 +14,8 @@
 // 2 * positions / chunk items, so all of them together have fewer than 2 * target.
 //
 // Shares (few rows): the positions of all tiles, in units of `step`, form one line
-// that is cut into `target / (hkv / hw)` pieces of equal length, one per workgroup
-// (and group of hw heads), or fewer of at least `min_chunk` units. A piece may hold the end of one tile, whole tiles, and the start of
+// that is cut into pieces of equal length, one per workgroup (and group of hw heads),
+// `target` workgroups in all, or fewer. A piece may hold the end of one tile, whole tiles, and the start of
 // another, so every workgroup has the same amount to read, whatever the lengths.
 //
 // What a workgroup computes of a cut tile goes to the workspace, as does a record
@@ -33,6 +33,7 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kAttnAlign = 64;   // `step` at most (a power of two): a tile's first position is rounded down to it
+constexpr int kWideBlocks = 8;   // (see attn_share)
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row's reference
 
 // What one workgroup works on.
@@ -229,10 +230,11 @@ struct AttnCut {
     return u < big ? u / (each + 1) : extra + (u - big) / each;
   }
 };
-// The share of workgroup w (of a group of heads): units [at, end) of the line, of which
-// `at` is unit `in_tile` of tile `tile` of sequence b; b is -1 where there is no share.
+// A workgroup's share: heads h .. h + hw - 1, units [at, end) of the line (piece w), of
+// which `at` is unit `in_tile` of tile `tile` of sequence b; b is -1 where there is none.
 struct AttnShare {
   AttnCut cut;
+  int h, hw, w;
   uint32_t at, end;
   int b, tile, in_tile;
   int row0, fresh, cached;    // of sequence b
@@ -246,8 +248,10 @@ struct ShareScan {
   AttnShare found;
 };
 
+// Workgroups go to the eight XCDs in turn: all heads of a piece to one of them, so that
+// its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
 template <int NT>
-__device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, uint32_t w, ShareScan<NT>& sh) {
+__device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // a thread's sequences; of up to NT, the prefix sum over them is the total as well
   uint32_t units0 = 0, all = 0;
@@ -278,11 +282,24 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, uint32_t w, S
     if (v < wave) before += sh.part[v];
     s.cut.units += sh.part[v];
   }
-  s.cut.pieces = min((uint32_t)max(p.target / (p.hkv / p.hw), 1), (s.cut.units + p.min_chunk - 1) / p.min_chunk);
-  if (w >= s.cut.pieces) {
+  s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
+  // With much to read, a wave per head and neighbouring heads together (p.hw). With fewer
+  // than kWideBlocks blocks per wave, all waves on one head: a quarter of the parts to
+  // join for the same time.
+  const bool wide = (unsigned long long)s.cut.units * (p.hkv / p.hw) >= (unsigned long long)kWideBlocks * p.target;
+  s.hw = wide ? p.hw : 1;
+  const int groups = wide ? p.hkv / p.hw : p.hkv, least = wide ? 1 : NT / 64;
+  const uint32_t at8 = blockIdx.x / 8;
+  s.h = at8 % groups * s.hw;
+  s.w = at8 / groups * 8 + blockIdx.x % 8;
+  s.cut.pieces = min((uint32_t)max(p.target / groups, 1), (s.cut.units + least - 1) / least);
+  if (blockIdx.x == 0 && tid == 0) *attn_record_count(p) = s.cut.pieces;
+  if (s.w >= s.cut.pieces) {
     s.b = -1;
     return s;
   }
+  if (s.h == 0 && tid == 0) attn_record(p, s.w)->parts = 0;
+  const uint32_t w = s.w;
   s.cut.each = s.cut.units / s.cut.pieces;
   s.cut.extra = s.cut.units % s.cut.pieces;
   s.at = s.cut.start(w);
@@ -339,7 +356,6 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, uint32_t w, S
   s.row0 = __builtin_amdgcn_readfirstlane(sh.found.row0);
   s.fresh = __builtin_amdgcn_readfirstlane(sh.found.fresh);
   s.cached = __builtin_amdgcn_readfirstlane(sh.found.cached);
-  s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
   s.cut.pieces = __builtin_amdgcn_readfirstlane(s.cut.pieces);
   s.cut.each = __builtin_amdgcn_readfirstlane(s.cut.each);
   s.cut.extra = __builtin_amdgcn_readfirstlane(s.cut.extra);

@@ -19,7 +19,7 @@ namespace qg {
 namespace {
 
 constexpr int JT = 256;
-constexpr int kRowsMost = 512, kRowsStep = 32, kRowsUnits = 1, kRowsHeads = 4;
+constexpr int kRowsMost = 512, kRowsStep = 32, kRowsHeads = 4;
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -148,17 +148,19 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   // sequence b has ceil(new_b * group / bm) tiles per key/value head, of at most `room` positions
   const long long tiles = rows / p.bm + p.batch, room = p.max_pages * p.page_size;
   if (few) {
-    p.min_chunk = kRowsUnits;
     attention_rows_shape(p, mt);
     const int groups = p.hkv / p.hw;
     p.target = std::max(std::min(p.target, kRowsMost), groups);
+    // pieces, at most: a wave per head (groups), or all waves on one head
     const long long units = (room + p.step - 1) / p.step;   // of a tile, at most
-    const long long shares = units < p.target ? std::min<long long>(p.target / groups, (tiles * units + p.min_chunk - 1) / p.min_chunk)
-                                              : p.target / groups;
-    const long long grid = (shares + 7) / 8 * 8 * groups;
-    if (grid > INT32_MAX || units > INT32_MAX / tiles) return hipErrorNotSupported;   // units are counted in 32 bits
+    if (units > INT32_MAX / tiles) return hipErrorNotSupported;   // units are counted in 32 bits
+    const long long wide = std::min<long long>(p.target / groups, tiles * units);
+    const long long narrow = std::min<long long>(std::max(p.target / p.hkv, 1), tiles * units);
+    const long long grid = std::max((wide + 7) / 8 * 8 * groups, (narrow + 7) / 8 * 8 * p.hkv);
+    if (grid > INT32_MAX) return hipErrorNotSupported;
     const hipError_t e = launch_attention_rows(p, mt, (unsigned)grid, stream);
-    return e != hipSuccess || shares <= 1 ? e : launch_join(p, shares, stream);   // one share has all its tiles whole
+    const long long pieces = std::max(wide, narrow);
+    return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
   }
   p.min_chunk = kTileMinChunk;
   p.target = std::max(kTileTarget, p.hkv);

@@ -464,25 +464,18 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 
 // Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
 template <int DP, int GRAN, int MT, int NW, int NST>
-__device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int c_first, int c_end, int slot,
-                                                           AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
+__device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int h, int hw, int c_first, int c_end,
+                                                           int slot, AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), blockIdx.x / 8 % (p.hkv / p.hw) * p.hw, p.hw, __builtin_amdgcn_readfirstlane(c_first),
+  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(hw),
+                                           __builtin_amdgcn_readfirstlane(c_first),
                                            __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds);
 }
 
 template <int DP, int GRAN, int MT, int NW, int NST>
 __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) {
   __shared__ AttnRowsLds<DP, GRAN, MT, NW, NST> lds;
-  // Workgroups go to the eight XCDs in turn: all heads of a share to one of them, so
-  // that its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
-  const int groups = p.hkv / p.hw;
-  const int h = blockIdx.x / 8 % groups * p.hw, w = blockIdx.x / 8 / groups * 8 + blockIdx.x % 8;
-  AttnShare s = attn_share<NW * 64>(p, w, lds.scan);
-  if (h == 0 && threadIdx.x == 0) {
-    if (w == 0) *attn_record_count(p) = gridDim.x / groups;
-    attn_record(p, w)->parts = 0;
-  }
+  AttnShare s = attn_share<NW * 64>(p, lds.scan);
   if (s.b < 0) return;
   while (true) {
     AttnItem it{};
@@ -498,18 +491,19 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
     const int c_first = t.start + s.in_tile * p.step, c_end = min(t.end, c_first + take * p.step);
     if (c_first < c_end) {                                     // a tile may end before its sequence's longest does
       const uint32_t last_unit = first_unit + ((t.end - t.start + p.step - 1) >> p.step_log2) - 1;
-      const uint32_t begin = s.cut.start(w);
+      const uint32_t begin = s.cut.start(s.w);
       // a share's first part goes to its slot 2 w, its last to 2 w + 1; those between are whole tiles
-      const int slot = first_unit >= begin && last_unit < s.end ? -1 : (2 * w + (s.at == begin ? 0 : 1)) * p.hkv + h;
-      if (first_unit < begin && h == 0 && threadIdx.x == 0) {
+      const int slot = first_unit >= begin && last_unit < s.end ? -1 : (2 * s.w + (s.at == begin ? 0 : 1)) * p.hkv + s.h;
+      if (first_unit < begin && s.h == 0 && threadIdx.x == 0) {
         const int w0 = s.cut.of(first_unit);
-        if (w == w0 + 1) {                                     // the tile's second share describes it for the join
+        if (s.w == w0 + 1) {                                     // the tile's second share describes it for the join
           const int first = 2 * w0 + (first_unit == s.cut.start(w0) ? 0 : 1);
-          *attn_record(p, w) = AttnRecord{(int)s.cut.of(last_unit) - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv, 2 * w * p.hkv, 2 * p.hkv, 1};
+          *attn_record(p, s.w) = AttnRecord{(int)s.cut.of(last_unit) - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv,
+                                            2 * s.w * p.hkv, 2 * p.hkv, 1};
         }
       }
-      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, h, p.hw, c_first, c_end, slot, lds))
-        attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, c_first, c_end, slot, &lds);
+      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, s.h, s.hw, c_first, c_end, slot, lds))
+        attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, s.hw, c_first, c_end, slot, &lds);
     }
     s.at += take;
     if (s.at >= s.end) return;
