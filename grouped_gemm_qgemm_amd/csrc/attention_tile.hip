@@ -38,15 +38,11 @@ namespace {
 constexpr int AW = 4;                // waves
 constexpr int TPG = 1024;            // page table entries held in LDS at a time
 
-// 16-byte chunk c of LDS row r (DP bf16 elements): the 16 rows of a read phase of
-// the key fragments, and the 4 x 64 bytes of a transposed read of values, meet
-// different banks
+// 16-byte chunk c of LDS row r (DP bf16 elements) lies at c ^ swz(r): the 16 rows of a
+// read phase of the key fragments, and the 4 x 64 bytes of a transposed read of
+// values, meet different banks
 template <int DP>
-__device__ __forceinline__ int swz_tk(int r) {
-  return DP >= 128 ? r & 15 : (r >> 1) & 7;
-}
-template <int DP>
-__device__ __forceinline__ int swz_tv(int r) {
+__device__ __forceinline__ int swz_t(int r) {
   return DP >= 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r >> 1) & 1) << 2 | ((r >> 2) & 3);
 }
 
@@ -132,6 +128,19 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   const size_t plane_scales = (size_t)p.pages * p.page_size * p.hkv * runs;
   const float* key_scales = FP8 ? p.scales + 2 * p.layer * plane_scales + (size_t)h * runs : nullptr;
   const uint32_t* my_pages = p.page_table + (size_t)it.b * p.max_pages;
+  const int row_scales = p.hkv * runs;
+  const bool by16 = p.page_size % 16 == 0;
+  // Where this lane's loads of a block come from, within 16 positions of one page. bf16:
+  // LDS position e = 64 (LD wave + k) + lane is row e / CH, chunk e % CH; e4m3: load k is
+  // row (k NT + tid) / LC, codes 16 ((k NT + tid) % LC) .. + 15.
+  constexpr int NV = FP8 ? LQ : LD;
+  const int e0 = FP8 ? tid : wave * LD * 64 + lane, ek = FP8 ? NT : 64, er = FP8 ? LC : CH;
+  uint32_t voff[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int e = e0 + k * ek, key = e / er, c = FP8 ? min(e % er * 16, p.d - 16) : ((e % er) ^ swz_t<DP>(key)) * 16;
+    voff[k] = (key & 15) * (uint32_t)row_bytes + c;
+  }
 
   float16_t acc[RT][ND];
   float m[RT], l[RT];     // reference of the weights' exponents (base 2), this lane's share of their sum
@@ -146,14 +155,16 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         for (int i = 0; i < 16; ++i) acc[rt][n][i] = 0.f;
     }
     // as many positions at a time as the list of pages covers
-    const int seg = (int)min((long long)it.chunk, (long long)(TPG - 1) * p.page_size / KB * KB);
+    const int seg = by16 ? it.chunk : (int)min((long long)it.chunk, (long long)(TPG - 1) * p.page_size / KB * KB);
     for (int s_first = c_first; s_first < c_end; s_first += seg) {
       const int s_end = min(c_end, s_first + seg);
-      const int page0 = fast_div(max(s_first, t.begin), p.div_mul, p.div_shift);
-      const int page1 = fast_div(s_end - 1, p.div_mul, p.div_shift);
-      __syncthreads();
-      for (int e = tid; e <= page1 - page0; e += NT) pages[e] = my_pages[page0 + e];
-      __syncthreads();
+      const int page0 = by16 ? 0 : fast_div(max(s_first, t.begin), p.div_mul, p.div_shift);
+      if (!by16) {
+        const int page1 = fast_div(s_end - 1, p.div_mul, p.div_shift);
+        __syncthreads();
+        for (int e = tid; e <= page1 - page0; e += NT) pages[e] = my_pages[page0 + e];
+      }
+      if (!by16 || chunks < CH) __syncthreads();
 
       // positions outside [begin, end) re-read one inside (their pages may not exist)
       auto row_of = [&](int pos) {
@@ -161,32 +172,89 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         const uint32_t pg = fast_div(x, p.div_mul, p.div_shift);
         return (size_t)pages[pg - page0] * p.page_size + (x - pg * p.page_size);
       };
+      // an offset of voff, for a position that is not in [begin, s_end)
+      auto clamped = [&](const Row16& r, int k) {
+        const int e = e0 + k * ek, key = e / er;
+        const int x = min(max(r.pos + (key & 15), t.begin), s_end - 1) - r.pos;
+        return voff[k] + (x - (key & 15)) * (uint32_t)row_bytes;
+      };
       // bf16: block i on its way into ring[at]
       auto issue = [&](int i, int at) {
+        const int first = s_first + KB * i;
+        if (by16) {
+          // a wave loads 16 positions (8 where a block has 32): one page
+          const int mine = wave * (KB / AW) & ~15;
+          const Row16 r = rows_of16(p, (page_list_t)my_pages, first + mine, t.begin, s_end);
+          const char* kbase = uniform(keys + r.row * row_bytes);
+          const char* vbase = uniform(kbase + plane_bytes);
+          const bool inside = first + mine >= t.begin && first + mine + 16 <= s_end;
+#pragma unroll
+          for (int k = 0; k < LD; ++k) {
+            const int e = (wave * LD + k) * 64;
+            const uint32_t off = inside ? voff[k] : clamped(r, k);
+            if (((e + lane) % CH ^ swz_t<DP>((e + lane) / CH)) < chunks) {
+              dma16(kbase, off, lds_addr(&ring[at][0][e]));
+              dma16(vbase, off, lds_addr(&ring[at][1][e]));
+            }
+          }
+          return;
+        }
 #pragma unroll
         for (int k = 0; k < LD; ++k) {
-          const int e0 = (wave * LD + k) * 64, e = e0 + lane, key = e / CH, c = e % CH;
-          const size_t off = row_of(s_first + KB * i + key) * row_bytes;
-          const int ck = c ^ swz_tk<DP>(key), cv = c ^ swz_tv<DP>(key);
-          if (ck < chunks) dma16_at(keys + off + ck * 16, lds_addr(&ring[at][0][e0]));
-          if (cv < chunks) dma16_at(keys + off + plane_bytes + cv * 16, lds_addr(&ring[at][1][e0]));
+          const int e = (wave * LD + k) * 64, key = (e + lane) / CH, c = (e + lane) % CH ^ swz_t<DP>(key);
+          const char* src = keys + row_of(first + key) * row_bytes + c * 16;
+          if (c < chunks) {
+            dma16_at(src, lds_addr(&ring[at][0][e]));
+            dma16_at(src + plane_bytes, lds_addr(&ring[at][1][e]));
+          }
         }
       };
       // e4m3: block i into registers, and from there into ring[at]
       u32x4_t stage[2][FP8 ? LQ : 1];
       float stage_s[FP8 ? LS : 1];
       auto fetch = [&](int i) {
+        const int first = s_first + KB * i;
+        if (by16) {
+          Row16 r[KB / 16];
+#pragma unroll
+          for (int g = 0; g < KB / 16; ++g) r[g] = rows_of16(p, (page_list_t)my_pages, first + 16 * g, t.begin, s_end);
+          const bool inside = first >= t.begin && first + KB <= s_end;
+#pragma unroll
+          for (int k = 0; k < LQ; ++k) {
+            constexpr int PER = 64 / LC;   // positions of a wave's load
+            const int g = (k * (NT / LC) + wave * PER) >> 4;
+            Row16 rk = r[0];
+#pragma unroll
+            for (int u = 1; u < KB / 16; ++u)
+              if (g == u) rk = r[u];
+            const char* base = uniform(keys + rk.row * row_bytes);
+            const uint32_t off = inside ? voff[k] : clamped(rk, k);
+            stage[0][k] = *reinterpret_cast<const u32x4_t*>(base + off);
+            stage[1][k] = *reinterpret_cast<const u32x4_t*>(base + plane_bytes + off);
+          }
+#pragma unroll
+          for (int k = 0; k < LS; ++k) {
+            const int e = min(k * NT + tid, 2 * KB * R - 1), plane = e / (KB * R), run = e / KB % R, key = e % KB;
+            Row16 rk = r[0];
+#pragma unroll
+            for (int u = 1; u < KB / 16; ++u)
+              if (key >> 4 == u) rk = r[u];
+            const int x = min(max(rk.pos + (key & 15), t.begin), s_end - 1) - rk.pos;
+            stage_s[k] = key_scales[plane * plane_scales + (rk.row + x) * row_scales + min(run, runs - 1)];
+          }
+          return;
+        }
 #pragma unroll
         for (int k = 0; k < LQ; ++k) {
           const int e = k * NT + tid, key = e / LC, c = e % LC;
-          const char* src = keys + row_of(s_first + KB * i + key) * row_bytes + min(c * 16, p.d - 16);
+          const char* src = keys + row_of(first + key) * row_bytes + min(c * 16, p.d - 16);
           stage[0][k] = *reinterpret_cast<const u32x4_t*>(src);
           stage[1][k] = *reinterpret_cast<const u32x4_t*>(src + plane_bytes);
         }
 #pragma unroll
         for (int k = 0; k < LS; ++k) {
           const int e = min(k * NT + tid, 2 * KB * R - 1), plane = e / (KB * R), run = e / KB % R, key = e % KB;
-          stage_s[k] = key_scales[plane * plane_scales + row_of(s_first + KB * i + key) * (p.hkv * runs) + min(run, runs - 1)];
+          stage_s[k] = key_scales[plane * plane_scales + row_of(first + key) * row_scales + min(run, runs - 1)];
         }
       };
       auto store = [&](int at) {
@@ -199,7 +267,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             uint32_t o[8];
 #pragma unroll
             for (int g = 0; g < 4; ++g) e4m3x4_to_bf16(stage[plane][k][g], o[2 * g], o[2 * g + 1]);
-            const int z = plane ? swz_tv<DP>(key) : swz_tk<DP>(key);
+            const int z = plane ? swz_t<DP>(key) : swz_t<DP>(key);
             ring[at][plane][key * CH + ((2 * c) ^ z)] = u32x4_t{o[0], o[1], o[2], o[3]};
             ring[at][plane][key * CH + ((2 * c + 1) ^ z)] = u32x4_t{o[4], o[5], o[6], o[7]};
           }
@@ -240,7 +308,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             for (int e = 0; e < 16; ++e) part[rt][e] = 0.f;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
-            const u32x4_t kf = lk[key * CH + ((2 * s + half) ^ swz_tk<DP>(key))];
+            const u32x4_t kf = lk[key * CH + ((2 * s + half) ^ swz_t<DP>(key))];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) part[rt] = mfma32x32x16_bf16(kf, qf[rt][s], part[rt]);
             if constexpr (FP8) {
@@ -341,8 +409,8 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         auto values = [&](int nb, int ks, int n) {
           const int m16 = lane & 15, c0 = n * 32 + 16 * ((lane >> 4) & 1) + 4 * (m16 & 3);
           const int key = nb * 32 + ks * 16 + 4 * half + (m16 >> 2);
-          const uint64_t w0 = lds_read_tr16(lv + (key * CH + ((c0 >> 3) ^ swz_tv<DP>(key))) * 16 + (c0 & 7) * 2);
-          const uint64_t w1 = lds_read_tr16(lv + ((key + 8) * CH + ((c0 >> 3) ^ swz_tv<DP>(key + 8))) * 16 + (c0 & 7) * 2);
+          const uint64_t w0 = lds_read_tr16(lv + (key * CH + ((c0 >> 3) ^ swz_t<DP>(key))) * 16 + (c0 & 7) * 2);
+          const uint64_t w1 = lds_read_tr16(lv + ((key + 8) * CH + ((c0 >> 3) ^ swz_t<DP>(key + 8))) * 16 + (c0 & 7) * 2);
           return u32x4_t{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
         };
         if (!SAFE || !masked) {

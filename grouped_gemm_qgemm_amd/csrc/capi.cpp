@@ -468,6 +468,7 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   if (B > INT32_MAX / 2 || S > INT32_MAX / 2 || Hq > INT32_MAX / 2 || T > (INT32_MAX / 2) / (Hq / Hkv) ||
       kv->max_pages_per_seq > (INT32_MAX / 2) / S)
     return QG_ERR_UNSUPPORTED;
+  if (Hkv > (1 << 26) / D) return QG_ERR_UNSUPPORTED;   // offsets within 16 cache rows are 32-bit
   qg::AttnArgs p{};
   p.out = static_cast<uint16_t*>(out->data);
   p.q = static_cast<const uint16_t*>(q->data);
