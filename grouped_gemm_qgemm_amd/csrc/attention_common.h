@@ -128,12 +128,70 @@ struct AttnScan {
   AttnItem found;
 };
 
+// Positions per chunk, from the sum over the tiles of the positions they cover
+// (target is a power of two).
+__device__ __forceinline__ int attn_chunk(const AttnArgs& p, unsigned long long cost) {
+  const unsigned long long even = (cost * (unsigned)p.hkv + p.target - 1) >> p.target_log2;
+  const int chunk = even < (unsigned long long)p.min_chunk ? p.min_chunk : even > INT32_MAX / 2 ? INT32_MAX / 2 : (int)even;
+  return __builtin_amdgcn_readfirstlane((chunk + p.step - 1) & -p.step);
+}
+__device__ __forceinline__ int attn_chunks(int span, int chunk) { return span <= chunk ? 1 : (span + chunk - 1) / chunk; }
+
 // Item `want` of the launch, for head h; all NT threads call it. Items are ordered
 // by sequence, then chunk, then tile (the last tiles, which see the most positions,
 // first). Workgroup 0 also writes the workspace's count of records.
 template <int NT>
 __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int h, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (p.batch <= 64) {
+    // every wave looks at all sequences, one per lane: no barrier. The longest sequences
+    // come first, so that the last workgroups to start have the least to do.
+    int row0 = 0, fresh = 0, len = -1;
+    if (lane < p.batch) {
+      row0 = (int)p.offs[lane];
+      fresh = (int)p.offs[lane + 1] - row0;
+      len = fresh + (int)p.cache_len[lane];
+    }
+    const int tiles = attn_tiles(p, fresh), span = attn_span(p, len);
+    unsigned long long all = lane < p.batch ? (unsigned long long)tiles * (unsigned)span : 0;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
+    const int chunk = attn_chunk(p, all);
+    const int ns = tiles ? attn_chunks(span, chunk) : 0;
+    int rank = lane < p.batch ? 0 : lane;
+    for (int b = 0; b < p.batch; ++b) {
+      const int other = __builtin_amdgcn_readlane(len, b);
+      if (lane < p.batch) rank += other > len || (other == len && b < lane);
+    }
+    const int from = __builtin_amdgcn_ds_permute(4 * rank, lane);   // the sequence of this rank
+    const int tl = __shfl(tiles, from), nl = __shfl(ns, from);
+    const int items = tl * nl, cuts = nl > 1 ? tl : 0, slots = cuts * nl * p.hkv;
+    int ii = items, is = slots, ic = cuts;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int vi = __shfl_up(ii, d), vs = __shfl_up(is, d), vc = __shfl_up(ic, d);
+      if (lane >= d) { ii += vi; is += vs; ic += vc; }
+    }
+    if (blockIdx.x == 0 && tid == 63) *attn_record_count(p) = ic;
+    const unsigned long long hit = __ballot(want < ii);
+    AttnItem it{};
+    it.b = -1;
+    if (!hit) return it;
+    const int at = __ffsll((long long)hit) - 1;
+    auto of = [&](int x) { return __builtin_amdgcn_readlane(x, at); };
+    const int local = want - of(ii - items), nt = of(tl);
+    it.b = of(from);
+    it.split = local / nt;
+    it.tile = nt - 1 - (local - it.split * nt);
+    it.slots = of(is - slots);
+    it.nsplit = of(nl);
+    it.chunk = chunk;
+    it.row0 = __builtin_amdgcn_readlane(row0, it.b);
+    it.fresh = __builtin_amdgcn_readlane(fresh, it.b);
+    it.cached = __builtin_amdgcn_readlane(len, it.b) - it.fresh;
+    it.record = of(ic - cuts) + it.tile;
+    return uniform(it);
+  }
   unsigned long long cost = 0;
   int row00 = 0, fresh0 = 0, len0 = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
@@ -153,9 +211,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
   cost = 0;
 #pragma unroll
   for (int w = 0; w < NT / 64; ++w) cost += sh.cost[w];
-  const unsigned long long even = (cost * (unsigned)p.hkv + p.target - 1) / (unsigned)p.target;
-  int chunk = even < (unsigned long long)p.min_chunk ? p.min_chunk : even > INT32_MAX / 2 ? INT32_MAX / 2 : (int)even;
-  chunk = (chunk + p.step - 1) & -p.step;
+  const int chunk = attn_chunk(p, cost);
 
   int base = 0, slot_base = 0, cut_base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
@@ -168,7 +224,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
         len = fresh + (int)p.cache_len[b];
       }
       tiles = attn_tiles(p, fresh);
-      if (tiles) ns = (attn_span(p, len) + chunk - 1) / chunk;
+      if (tiles) ns = attn_chunks(attn_span(p, len), chunk);
     }
     const int items = tiles * ns, cuts = ns > 1 ? tiles : 0, slots = cuts * ns * p.hkv;
     int ii = items, is = slots, ic = cuts;
@@ -195,7 +251,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int
     __syncthreads();
     if (want < base && blockIdx.x > 0) break;
   }
-  if (blockIdx.x == 0 && tid == 0) reinterpret_cast<int*>(p.workspace)[0] = cut_base;
+  if (blockIdx.x == 0 && tid == 0) *attn_record_count(p) = cut_base;
   const AttnItem it = uniform(sh.found);
   return it;
 }
@@ -253,11 +309,13 @@ struct ShareScan {
 template <int NT>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const bool one_wave = p.batch <= 64;   // every wave looks at all sequences, one per lane: no barrier
+  const int me = one_wave ? lane : tid;
   // a thread's sequences; of up to NT, the prefix sum over them is the total as well
   uint32_t units0 = 0, all = 0;
   int row00 = 0, fresh0 = 0, len0 = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NT) {
-    const int b = b0 + tid;
+    const int b = b0 + me;
     if (b < p.batch) {
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
@@ -272,15 +330,19 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
     const uint32_t v = __shfl_up(incl, d);
     if (lane >= d) incl += v;
   }
-  if (lane == 63) sh.part[wave] = incl;
-  if (tid == 0) sh.found.b = -1;
-  __syncthreads();
   AttnShare s{};
   uint32_t before = 0;
+  if (one_wave) {
+    s.cut.units = __builtin_amdgcn_readlane(incl, 63);
+  } else {
+    if (lane == 63) sh.part[wave] = incl;
+    if (tid == 0) sh.found.b = -1;
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < NT / 64; ++v) {
-    if (v < wave) before += sh.part[v];
-    s.cut.units += sh.part[v];
+    for (int v = 0; v < NT / 64; ++v) {
+      if (v < wave) before += sh.part[v];
+      s.cut.units += sh.part[v];
+    }
   }
   s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
   // With much to read, a wave per head and neighbouring heads together (p.hw). With fewer
@@ -304,6 +366,18 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
   s.cut.extra = s.cut.units % s.cut.pieces;
   s.at = s.cut.start(w);
   s.end = s.cut.start(w + 1);
+  if (one_wave) {
+    const int at = __ffsll((long long)__ballot(s.at < incl)) - 1;
+    const uint32_t local = s.at - __builtin_amdgcn_readlane(incl - all, at);
+    s.b = at;
+    s.row0 = __builtin_amdgcn_readlane(row00, at);
+    s.fresh = __builtin_amdgcn_readlane(fresh0, at);
+    s.cached = __builtin_amdgcn_readlane(len0, at) - s.fresh;
+    const uint32_t un = attn_units(p, s.fresh + s.cached);
+    s.tile = local < un ? 0 : local / un;
+    s.in_tile = local - s.tile * un;
+    return s;
+  }
   auto look = [&](int b, uint32_t first, uint32_t units, int row0, int fresh, int len) {
     if (s.at >= first && s.at - first < units) {
       const uint32_t un = attn_units(p, len), local = s.at - first;

@@ -106,18 +106,21 @@ static hipError_t launch_join(const AttnArgs& p, long long cut, hipStream_t stre
   return hipGetLastError();
 }
 
+static int log2_of(int64_t x) {
+  int k = 0;
+  while (((int64_t)1 << k) < x) ++k;
+  return k;
+}
+
+// items of the kernel for many rows: a power of two, and at least one per head
+static int tile_target(int64_t hkv) { return std::max(kTileTarget, 1 << log2_of(hkv)); }
+
 int64_t attention_paged_workspace(int64_t T, int64_t batch, int64_t hq, int64_t hkv, int64_t d) {
   (void)T; (void)batch; (void)hq;
   // two slots per share and head
-  const int64_t rt = std::max<int64_t>(kRowsMost, hkv), tt = std::max<int64_t>(kTileTarget, hkv);
+  const int64_t rt = std::max<int64_t>(kRowsMost, hkv), tt = tile_target(hkv);
   return std::max(attn_header_floats((int)rt) + 2 * kRowsHeads * rt * attn_slot_floats(32, dp_of(d)),
                   attn_header_floats((int)tt) + 2 * tt * attn_slot_floats(128, dp_of(d)));
-}
-
-static int log2_of(int x) {
-  int k = 0;
-  while ((1 << k) < x) ++k;
-  return k;
 }
 
 // x / d for x < 2^31 as (umulhi(x, mul) + x) >> shift
@@ -163,7 +166,8 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
   }
   p.min_chunk = kTileMinChunk;
-  p.target = std::max(kTileTarget, p.hkv);
+  p.target = tile_target(p.hkv);
+  p.target_log2 = log2_of(p.target);
   // Items: at most target / hkv + tiles (a chunk is at least the work over the target),
   // and each tile has as many as the page table has room for. Workgroups past the last
   // item return.

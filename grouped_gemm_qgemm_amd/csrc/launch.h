@@ -123,7 +123,7 @@ struct AttnArgs {
   // (attention_common.h); bm and step are powers of two
   uint32_t div_mul = 0, div_shift = 0, group_mul = 0, group_shift = 0;
   int bm = 0, bm_log2 = 0, step = 0, step_log2 = 0, window_span = 0;
-  int target = 0, min_chunk = 0, hw = 1;
+  int target = 0, target_log2 = 0, min_chunk = 0, hw = 1;
 };
 
 // Decode-shaped W4A16 (M <= 16).
