@@ -415,7 +415,7 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
   if (result->shape[0] != 2 || free_count->shape[0] != 1) return QG_ERR_SHAPE;
   if (page_size <= 0) return QG_ERR_INVALID_ARG;
   const int64_t F = free_pages->shape[0], T = slot_map ? slot_map->shape[0] : 0;
-  if (B > qg::kTablesMaxBatch || W > INT32_MAX / page_size || F > INT32_MAX || T > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (B > qg::kTablesMaxBatch || W >= INT32_MAX / page_size || F > INT32_MAX || T > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (B == 0) return QG_OK;
   // a slot map without elements still bounds the number of tokens
   static int32_t none;

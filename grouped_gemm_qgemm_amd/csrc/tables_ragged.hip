@@ -12,8 +12,9 @@
 // where first_b counts the new pages of the sequences before b. Two prefix sums
 // over the sequences, then independent writes. All of it moves a few bytes per
 // token, so a call is bound by its latency: one launch, in which every workgroup
-// repeats the prefix sums (2 x 4 bytes per sequence, from L2) and writes its
-// share of the outputs. Nothing that one workgroup writes is read by another:
+// repeats the prefix sums (2 x 4 bytes per sequence, from L2; totals in 64 bits,
+// so that lengths which are too long are seen as such) and writes its share of the
+// outputs. Nothing that one workgroup writes is read by another:
 // entries added by this call are taken from the free stack again where a
 // token's slot needs them.
 #include "device_common.h"
@@ -23,9 +24,10 @@ namespace qg {
 
 namespace {
 
-constexpr int TT = 1024;             // threads per workgroup
+constexpr int TT = 256;              // threads per workgroup
 constexpr int TSEQ = kTablesMaxBatch;
-constexpr int TPER = TSEQ / TT;      // consecutive sequences per thread, at most
+constexpr int TLD = 8;               // sequences a thread loads at a time
+constexpr int TTOK = 4;              // consecutive tokens per thread and pass: one search, one 16-byte store
 
 // last b with first[b] <= x: among sequences that share a start, the one that is
 // not empty
@@ -44,36 +46,55 @@ __global__ __launch_bounds__(TT) void tables_ragged_kernel(
     uint32_t* __restrict__ offsets, int32_t* __restrict__ slots, uint32_t* __restrict__ table,
     uint32_t* __restrict__ result, const uint32_t* __restrict__ cached, const uint32_t* __restrict__ fresh,
     const uint32_t* __restrict__ free_pages, const uint32_t* __restrict__ free_count, int batch, int max_pages,
-    uint32_t free_len, long long slot_len, uint32_t page_size) {
+    uint32_t free_len, long long slot_len, uint32_t page_size, uint32_t div_mul, uint32_t div_shift) {
   __shared__ uint32_t s_tok[TSEQ], s_pg[TSEQ];
   __shared__ unsigned long long w_tok[TT / 64], w_pg[TT / 64];
   __shared__ int s_bad;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t count = free_count[0];
+  // x / page_size, for positions that the page table has room for (below 2^31)
+  auto page_of = [&](uint32_t x) { return (__umulhi(x, div_mul) + x) >> div_shift; };
   if (tid == 0) s_bad = 0;
   __syncthreads();
 
-  // sums in 64 bits, so that lengths which are too long are seen as such
-  const int per = (batch + TT - 1) / TT;
-  unsigned long long tok = 0, pg = 0;
-  uint32_t n_own[TPER], p_own[TPER];
+  const unsigned long long room = (unsigned long long)max_pages * page_size;   // below 2^31
   bool bad = false;
+  for (int b0 = tid; b0 < batch; b0 += TLD * TT) {   // new tokens and pages of each sequence
+    uint32_t n[TLD], c[TLD];
 #pragma unroll
-  for (int k = 0; k < TPER; ++k) {
-    const int b = tid * per + k;
-    n_own[k] = p_own[k] = 0;
-    if (k < per && b < batch) {
-      const unsigned long long c = cached[b], n = fresh[b];
-      if (n != 0) {   // a sequence without new tokens is left alone, whatever its length
-        const unsigned long long need = (c + n + page_size - 1) / page_size;
-        bad |= need > (unsigned long long)max_pages;
-        n_own[k] = (uint32_t)n;
-        p_own[k] = (uint32_t)(need - (c + page_size - 1) / page_size);
-        tok += n;
-        pg += p_own[k];
+    for (int k = 0; k < TLD; ++k) {
+      const int b = min(b0 + k * TT, batch - 1);
+      n[k] = fresh[b];
+      c[k] = cached[b];
+    }
+#pragma unroll
+    for (int k = 0; k < TLD; ++k) {
+      uint32_t more = 0;
+      const unsigned long long len = (unsigned long long)c[k] + n[k];
+      if (n[k] == 0) {
+        // a sequence without new tokens is left alone, whatever its length
+      } else if (len <= room) {
+        more = page_of(c[k] + n[k] + page_size - 1) - page_of(c[k] + page_size - 1);
+      } else {   // past what page_of takes
+        bad = true;
+        const unsigned long long m = (len + page_size - 1) / page_size - ((unsigned long long)c[k] + page_size - 1) / page_size;
+        more = (uint32_t)min(m, 0xFFFFFFFFull);
+      }
+      if (b0 + k * TT < batch) {
+        s_tok[b0 + k * TT] = n[k];
+        s_pg[b0 + k * TT] = more;
       }
     }
   }
   if (bad) s_bad = 1;
+  __syncthreads();
+  // their starts: each thread sums consecutive sequences
+  const int per = (batch + TT - 1) / TT;
+  unsigned long long tok = 0, pg = 0;
+  for (int b = tid * per; b < min(batch, tid * per + per); ++b) {
+    tok += s_tok[b];
+    pg += s_pg[b];
+  }
   unsigned long long it = tok, ip = pg;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -90,19 +111,15 @@ __global__ __launch_bounds__(TT) void tables_ragged_kernel(
     pages += w_pg[w];
   }
   unsigned long long xt = bt + it - tok, xp = bp + ip - pg;
-#pragma unroll
-  for (int k = 0; k < TPER; ++k) {
-    const int b = tid * per + k;
-    if (k < per && b < batch) {
-      s_tok[b] = (uint32_t)xt;
-      s_pg[b] = (uint32_t)xp;
-      xt += n_own[k];
-      xp += p_own[k];
-    }
+  for (int b = tid * per; b < min(batch, tid * per + per); ++b) {
+    const uint32_t n = s_tok[b], more = s_pg[b];
+    s_tok[b] = (uint32_t)xt;
+    s_pg[b] = (uint32_t)xp;
+    xt += n;
+    xp += more;
   }
   __syncthreads();
 
-  const uint32_t count = free_count[0];
   uint32_t status = 0;
   if (count > free_len || pages > count) status |= 1;
   if (s_bad) status |= 2;
@@ -117,27 +134,59 @@ __global__ __launch_bounds__(TT) void tables_ragged_kernel(
   for (uint32_t b = gid; b <= (uint32_t)batch; b += threads) offsets[b] = b < (uint32_t)batch ? s_tok[b] : (uint32_t)tokens;
   for (uint32_t j = gid; j < (uint32_t)pages; j += threads) {
     const int b = owner(s_pg, batch, j);
-    const uint32_t held = (cached[b] + page_size - 1) / page_size;
+    const uint32_t held = page_of(cached[b] + page_size - 1);
     table[(size_t)b * max_pages + held + (j - s_pg[b])] = free_pages[count - 1 - j];
   }
   if (!slots) return;
-  for (uint32_t t = gid; t < (uint32_t)tokens; t += threads) {
-    const int b = owner(s_tok, batch, t);
-    const uint32_t c = cached[b], pos = c + (t - s_tok[b]);
-    const uint32_t held = (c + page_size - 1) / page_size;
-    const uint32_t col = pos / page_size;
-    const uint32_t page = col < held ? table[(size_t)b * max_pages + col] : free_pages[count - 1 - (s_pg[b] + col - held)];
-    slots[t] = (int32_t)(page * page_size + pos % page_size);
+  const uint32_t all = (uint32_t)tokens;
+  for (uint32_t t0 = gid * TTOK; t0 < all; t0 += threads * TTOK) {
+    int b = owner(s_tok, batch, t0);
+    int32_t v[TTOK];
+    uint32_t c = cached[b], pos = c + (t0 - s_tok[b]), next = b + 1 < batch ? s_tok[b + 1] : all;
+    uint32_t held = page_of(c + page_size - 1), seen = ~0u, page = 0;
+#pragma unroll
+    for (int k = 0; k < TTOK; ++k) {
+      const uint32_t t = t0 + k;
+      if (t < all) {
+        if (t >= next) {   // on to the next sequence that has tokens
+          do {
+            ++b;
+            next = b + 1 < batch ? s_tok[b + 1] : all;
+          } while (t >= next);
+          pos = c = cached[b];
+          held = page_of(c + page_size - 1);
+          seen = ~0u;
+        }
+        const uint32_t col = page_of(pos);
+        if (col != seen) {
+          seen = col;
+          page = col < held ? table[(size_t)b * max_pages + col] : free_pages[count - 1 - (s_pg[b] + col - held)];
+        }
+        v[k] = (int32_t)(page * page_size + (pos - col * page_size));
+        ++pos;
+      }
+    }
+    if (t0 + TTOK <= all) {
+      *reinterpret_cast<int4*>(slots + t0) = int4{v[0], v[1], v[2], v[3]};
+    } else {
+#pragma unroll
+      for (int k = 0; k < TTOK; ++k)
+        if (t0 + k < all) slots[t0 + k] = v[k];
+    }
   }
 }
 
 hipError_t launch_tables_ragged(const TablesArgs& p, hipStream_t stream) {
-  // one workgroup per 4096 tokens (four passes of its threads), at most two per CU
-  const long long want = (p.slot_len + 4 * TT - 1) / (4 * TT);
+  // x / page_size for x < 2^31 as (umulhi(x, mul) + x) >> shift
+  uint32_t shift = 0;
+  while ((1u << shift) < (uint32_t)p.page_size) ++shift;
+  const uint32_t mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)p.page_size)) / (uint64_t)p.page_size) + 1);
+  // a workgroup per 2048 tokens (two passes of its threads), at most two per CU (64 KB of LDS)
+  const long long want = (p.slot_len + 2 * TTOK * TT - 1) / (2 * TTOK * TT);
   const int grid = (int)(want < 1 ? 1 : want > 2 * p.num_cus ? 2 * p.num_cus : want);
   tables_ragged_kernel<<<grid, TT, 0, stream>>>(p.offsets, p.slots, p.table, p.result, p.cached, p.fresh, p.free_pages,
                                                 p.free_count, p.batch, p.max_pages, (uint32_t)p.free_len, p.slot_len,
-                                                (uint32_t)p.page_size);
+                                                (uint32_t)p.page_size, mul, shift);
   return hipGetLastError();
 }
 

@@ -385,8 +385,8 @@ qg_status kv_matmul_ragged_paged_scale(const qg_tensor* hidden, const qg_tensor*
  *   4  there are more tokens than slot_map has elements (2^31 - 1 without one)
  * and then nothing but `result` is written, with result[0] = free_count[0]: the
  * caller looks at it before the tables are used. Page ids are not checked; they
- * are below 2^31 / S. cache_lengths is not updated. B above 8192, or W * S above
- * 2^31 - 1, is QG_ERR_UNSUPPORTED; B = 0 is a no-op.
+ * are below 2^31 / S. cache_lengths is not updated. B above 8192, or (W + 1) * S
+ * above 2^31 - 1, is QG_ERR_UNSUPPORTED; B = 0 is a no-op.
  */
 qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tensor* slot_map,
                               const qg_tensor* page_table, const qg_tensor* result,
