@@ -32,7 +32,6 @@ typedef int i32x2v_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kAttnAlign = 64;   // `step` at most (a power of two): a tile's first position is rounded down to it
 constexpr int kWideBlocks = 8;   // (see attn_share)
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row's reference
 
@@ -272,7 +271,7 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem&
   t.t_last = over_group(p, t.r_first + t.r_count - 1);
   t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
   t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
-  t.start = t.begin & -p.step;   // so that the first unit, or chunk, holds a position that is seen
+  t.start = t.begin & -p.step;   // so that the first unit, or chunk, holds a position that is seen (step: a power of two)
   return t;
 }
 
@@ -467,6 +466,17 @@ template <int N>
 __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
+// until the loads of at most min(left, N) blocks of LB loads each are in flight
+template <int LB, int N>
+__device__ __forceinline__ void wait_blocks(int left) {
+  if constexpr (N == 0) {
+    wait_loads<0>();
+  } else {
+    if (left >= N) wait_loads<N * LB>();
+    else wait_blocks<LB, N - 1>(left);
+  }
+}
+
 // until this wave's LDS reads have returned (before a load into the same place)
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 

@@ -135,8 +135,8 @@ static void set_shape(AttnArgs& p, int bm, int step) {
   p.bm_log2 = log2_of(bm);
   p.step = step;
   p.step_log2 = log2_of(step);
-  // a tile has tokens t .. t + (bm - 1) / group + 1 at most
-  const long long span = (long long)p.window + (bm - 1) / p.group + 1 + kAttnAlign;
+  // a tile has tokens t .. t + (bm - 1) / group + 1 at most, and starts up to step - 1 early
+  const long long span = (long long)p.window + (bm - 1) / p.group + 1 + step;
   p.window_span = (int)std::min<long long>(span, INT32_MAX);
 }
 
@@ -155,8 +155,8 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const int groups = p.hkv / p.hw;
     p.target = std::max(std::min(p.target, kRowsMost), groups);
     // pieces, at most: a wave per head (groups), or all waves on one head
+    while ((room + p.step - 1) / p.step > INT32_MAX / tiles) set_shape(p, p.bm, 2 * p.step);   // units are counted in 32 bits
     const long long units = (room + p.step - 1) / p.step;   // of a tile, at most
-    if (units > INT32_MAX / tiles) return hipErrorNotSupported;   // units are counted in 32 bits
     const long long wide = std::min<long long>(p.target / groups, tiles * units);
     const long long narrow = std::min<long long>(std::max(p.target / p.hkv, 1), tiles * units);
     const long long grid = std::max((wide + 7) / 8 * 8 * groups, (narrow + 7) / 8 * 8 * p.hkv);

@@ -35,17 +35,6 @@ __device__ __forceinline__ int swz_r(int r) {
   return CH >= 16 ? (r & 7) | ((r >> 4) & 1) << 3 : CH == 8 ? ((r >> 1) & 3) | ((r >> 4) & 1) << 2 : ((r >> 2) & 1) | ((r >> 4) & 1) << 1;
 }
 
-// until the loads of at most min(left, N) blocks of LB loads each are in flight
-template <int LB, int N>
-__device__ __forceinline__ void wait_blocks(int left) {
-  if constexpr (N == 0) {
-    wait_loads<0>();
-  } else {
-    if (left >= N) wait_loads<N * LB>();
-    else wait_blocks<LB, N - 1>(left);
-  }
-}
-
 template <int DP, int GRAN, int MT, int NW, int NST>
 struct AttnRowsLds {
   static constexpr int TILE = 2 * DP * (GRAN > 0 ? 1 : 2);   // 16-byte chunks of a block's keys (or values)
@@ -488,7 +477,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
     const int un = attn_units(p, s.fresh + s.cached);          // the tile's units: [first_unit, first_unit + un)
     const uint32_t first_unit = s.at - s.in_tile;
     const int take = min((int)(s.end - s.at), un - s.in_tile);
-    const int c_first = t.start + s.in_tile * p.step, c_end = min(t.end, c_first + take * p.step);
+    // (a tile's first unit may begin with positions, and pages, that nobody sees)
+    const int from = t.start + s.in_tile * p.step, c_first = max(from, t.begin & ~31), c_end = min(t.end, from + take * p.step);
     if (c_first < c_end) {                                     // a tile may end before its sequence's longest does
       const uint32_t last_unit = first_unit + ((t.end - t.start + p.step - 1) >> p.step_log2) - 1;
       const uint32_t begin = s.cut.start(s.w);

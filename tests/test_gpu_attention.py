@@ -127,10 +127,31 @@ def test_lengths(lib, gpu, new, history, gran):
     check(lib, synth.attention_inputs(14, new, history, hq=4, hkv=1, d=128, gran=gran, spare_rows=1))
 
 
-@pytest.mark.parametrize("batch", [63, 64, 65, 200])
-def test_batches(lib, gpu, batch):
+@pytest.mark.parametrize("batch", [63, 64, 65, 200, 300, 600])
+@pytest.mark.parametrize("hq,hkv,dim", [(4, 2, 64), (9, 3, 64), (2, 1, 256), (40, 1, 64)])
+def test_batches(lib, gpu, batch, hq, hkv, dim):
+    """From one sequence per lane to several per thread, in both kernels (40 rows per token: the
+    one for chunks)."""
     rng = np.random.default_rng(batch)
-    check(lib, synth.attention_inputs(15, rng.integers(0, 3, batch), rng.integers(0, 90, batch), hq=4, hkv=2, d=64))
+    check(lib, synth.attention_inputs(15, rng.integers(0, 3, batch), rng.integers(0, 90, batch), hq=hq, hkv=hkv, d=dim))
+
+
+def test_a_page_table_far_wider_than_the_sequences(lib, gpu):
+    """Work is counted by what the table has room for where only that is known on the host."""
+    d = synth.attention_inputs(36, [1, 2, 1], [90, 700, 3], hq=8, hkv=4, d=64, page=16)
+    wide = np.full((3, 1 << 20), 0xFFFFFFFF, np.uint32)
+    wide[:, :d.page_table.shape[1]] = d.page_table
+    check(lib, dataclasses.replace(d, page_table=wide))
+    d = synth.attention_inputs(37, [100, 2, 70], [90, 700, 3], hq=8, hkv=4, d=64, page=16)
+    wide = np.full((3, 1 << 20), 0xFFFFFFFF, np.uint32)
+    wide[:, :d.page_table.shape[1]] = d.page_table
+    check(lib, dataclasses.replace(d, page_table=wide), window=50)
+
+
+def test_the_widest_window_is_none(lib, gpu):
+    for new in ([2, 1], [100, 1]):
+        d = synth.attention_inputs(38, new, [300, 40], hq=4, hkv=2, d=64)
+        assert np.array_equal(run(lib, d, 0.125, True, 2**31 - 1), run(lib, d, 0.125))
 
 
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 64, 100, 5000])
