@@ -296,6 +296,11 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         const u32x4_t* lk = ring[at][0];
         const char* lv = reinterpret_cast<const char*>(ring[at][1]);
 
+        // Two workgroups share a CU (bf16, heads up to 128): the one at its MFMAs goes first, so
+        // that the other's softmax fills in behind it instead of beside it (prompt of 8192:
+        // 588 -> 559 us; with e4m3's longer softmax, or one workgroup per CU, it costs 1 to 6 %).
+        constexpr bool FIRST = !FP8 && DP <= 128;
+        if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         // scores: register i of block nb holds position k0 + 32 nb + 8 (i / 4) + 4 half + i % 4
         float16_t sc[RT][NB];
 #pragma unroll
@@ -334,6 +339,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             for (int rt = 0; rt < RT; ++rt) sc[rt][nb] = part[rt];
           }
         }
+        if constexpr (FIRST) __builtin_amdgcn_s_setprio(0);
         const bool masked = uniform((p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
                                     k0 + KB > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end));
         if (masked) {
@@ -413,6 +419,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           const uint64_t w1 = lds_read_tr16(lv + ((key + 8) * CH + ((c0 >> 3) ^ swz_t<DP>(key + 8))) * 16 + (c0 & 7) * 2);
           return u32x4_t{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
         };
+        if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         if (!SAFE || !masked) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -461,6 +468,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
                 }
               }
         }
+        if constexpr (FIRST) __builtin_amdgcn_s_setprio(0);
         if constexpr (FP8) {
           if (i + 1 < blocks) store(at ^ 1);
         }
