@@ -346,7 +346,8 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
   s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
   // With much to read, a wave per head and neighbouring heads together (p.hw). With fewer
   // than kWideBlocks blocks per wave, all waves on one head: a quarter of the parts to
-  // join for the same time.
+  // join for the same time (single tokens, bf16: 8 sequences of 500 positions 16 us against
+  // 20, 16 of 2000 38 to 40 either way, 64 of 1 to 8192 222 us against 209).
   const bool wide = (unsigned long long)s.cut.units * (p.hkv / p.hw) >= (unsigned long long)kWideBlocks * p.target;
   s.hw = wide ? p.hw : 1;
   const int groups = wide ? p.hkv / p.hw : p.hkv, least = wide ? 1 : NT / 64;

@@ -8,7 +8,8 @@
 //
 // It is a second launch on the same stream rather than the task of the last
 // part to finish: that needs counters which every call must find at zero, and
-// ordering between the XCDs' caches within a kernel.
+// ordering between the XCDs' caches within a kernel. It takes 3 to 4 us where nothing or
+// little was cut and 6 to 11 us after a decode step of 64 sequences.
 #include <algorithm>
 #include <type_traits>
 
@@ -20,6 +21,9 @@ namespace {
 
 constexpr int JT = 256;
 constexpr int kRowsMost = 512, kRowsStep = 32, kRowsHeads = 4;
+// Items of the kernel for many rows, two per CU (one per CU: 1000 tokens after 32000 688 us
+// against 538; four: eight prompts of 1 to 1024 tokens 75 us against 63), of at least 256
+// positions (128 or 512: within 2 %).
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -145,8 +149,17 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   divide_by(p.page_size, p.div_mul, p.div_shift);
   divide_by(p.group, p.group_mul, p.group_shift);
   const long long rows = p.T * p.group;
-  const bool few = rows <= 32LL * p.batch;
+  // The kernel for few rows takes up to 16 rows per sequence and head on average (64
+  // sequences of one token: 207 us, 1.5 times that in tiles of 128 rows on bf16 and twice
+  // on e4m3), and up to 32 where there are many sequences (32 of 6 tokens on 4000
+  // positions, 4 heads to one: bf16 132 against 135 us, e4m3 90 against 125; on 500
+  // positions 28 against 37 and 33 against 39). With fewer, each is cut into many parts,
+  // whose records of 32 rows cost more than half-empty tiles (8 sequences: bf16 40 us
+  // against 52, e4m3 46 against 52), except for e4m3 heads of 256, which the kernel for
+  // many rows is slow at (126 us against 84). Beyond 32 rows it loses (32 sequences of 16
+  // tokens: bf16 191 us against 142, e4m3 141 against 133).
   const int mt = rows > 16LL * p.batch ? 2 : 1;
+  const bool few = mt == 1 || (rows <= 32LL * p.batch && (4LL * p.batch * p.hkv > p.num_cus || (p.fp8 && p.d > 128)));
   set_shape(p, few ? 16 * mt : 128, few ? kRowsStep : kTileStep);
   // sequence b has ceil(new_b * group / bm) tiles per key/value head, of at most `room` positions
   const long long tiles = rows / p.bm + p.batch, room = p.max_pages * p.page_size;

@@ -442,3 +442,42 @@ def test_a_window_that_starts_anywhere_in_a_block(lib, gpu, page, history):
     for b in range(3):
         d.page_table[b, :(int(d.cache_lengths[b]) - 1499) // page] = 0xFFFFFFFF
     compare(d, run(lib, d, 0.125, True, 1500), ref)
+
+
+def _drafts(batch, most, group):
+    """New tokens of `batch` sequences whose rows per key/value head are 17 to 32 on average:
+    the two row tiles of the kernel for few rows, which takes them where sequences are many."""
+    new = [most, 0, 1] + [24 // group] * (batch - 3)
+    assert 16 * batch < sum(new) * group <= 32 * batch
+    return new
+
+
+@pytest.mark.parametrize("gran,dim", [(0, 40), (0, 64), (0, 128), (0, 256), (32, 64), (64, 64), (32, 128), (64, 128), (128, 128),
+                                      (32, 192), (32, 256), (64, 256), (128, 256)])
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("batch", [33, 70])
+def test_drafts_of_many_sequences(lib, gpu, gran, dim, window, batch):
+    rng = np.random.default_rng(dim + gran)
+    d = synth.attention_inputs(38, _drafts(batch, 9, 4), rng.integers(0, 300, batch), hq=8, hkv=2, d=dim, gran=gran, spare_rows=2)
+    check(lib, d, window=window)
+
+
+@pytest.mark.parametrize("batch,hkv", [(4, 16), (5, 16), (8, 8), (9, 8), (65, 1), (64, 1)])
+@pytest.mark.parametrize("gran,dim", [(0, 64), (64, 256)])
+def test_drafts_at_the_change_of_kernels(lib, gpu, batch, hkv, gran, dim):
+    check(lib, synth.attention_inputs(39, _drafts(batch, 20, 4), [200 + 7 * i for i in range(batch)], hq=4 * hkv, hkv=hkv, d=dim,
+                                      gran=gran))
+
+
+@pytest.mark.parametrize("gran,dim", [(0, 64), (0, 128), (0, 256), (32, 64), (32, 256), (128, 128)])
+@pytest.mark.parametrize("plane", [0, 1])
+@pytest.mark.parametrize("window", [0, 9])
+def test_nan_among_drafts_of_many_sequences(lib, gpu, gran, dim, plane, window):
+    d = synth.attention_inputs(40, _drafts(34, 40, 4), [70] + [5 + 2 * i for i in range(33)], hq=8, hkv=2, d=dim, page=16, gran=gran)
+    at = 70 + 17
+    page, slot = d.page_table[0, at // 16], at % 16
+    d.blocks[1, plane, page, slot, :, 5] = 0x7F if gran else 0x7FC0
+    ref = exact(d, 0.125, True, window)
+    got = run(lib, d, 0.125, True, window)
+    compare(d, got, ref)
+    assert np.isfinite(bf16v(got)[:17]).all() and np.isfinite(bf16v(got)[40:]).all()
