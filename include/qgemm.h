@@ -38,7 +38,8 @@
  *     product, returns QG_ERR_UNSUPPORTED.
  *   - Outputs must not alias inputs. Calls on different streams may run
  *     concurrently; the library holds no mutable global state besides a cache of
- *     device properties.
+ *     device properties. attention_ragged_paged's workspace belongs to one call
+ *     at a time.
  */
 #ifndef QGEMM_H
 #define QGEMM_H
