@@ -510,7 +510,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
       off = 0;
 #pragma unroll
       for (int w = 0; w < AW; ++w) off |= lds.w_off[w];
-      if (off) return true;
+      if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
     }
   }
 
