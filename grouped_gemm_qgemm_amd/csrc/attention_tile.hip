@@ -25,15 +25,15 @@
 // are fp32. The one rounding inside is that of the probabilities to bf16, which
 // the MFMA takes (at most 2^-8 of each, as the output's own rounding).
 //
-// Measured (heads of 128, 32 on 8): a prompt of 8192 in 559 us, 985 TFLOP/s over the
-// pairs that see each other, MFMA busy 49 % of all SIMD cycles; 1000 tokens after a
-// history of 32000 in 524 us, 1.02 PFLOP/s (a large bf16 library product: 1.15 to
-// 1.2). 64 rows per wave, which would halve the LDS reads, leaves one wave per SIMD
+// Measured (heads of 128, 32 on 8): a prompt of 8192 in 566 us, 971 TFLOP/s over the
+// pairs that see each other; 1000 tokens after a history of 32000 in 549 us, 970 TFLOP/s
+// (a large bf16 library product: 1.15 to 1.2 PFLOP/s); eight prompts of 1 to 1024 tokens
+// 43 us. 64 rows per wave, which would halve the LDS reads, leaves one wave per SIMD
 // and accumulators that the compiler moves in and out of AGPRs: 280 TFLOP/s.
-// e4m3 caches reach 575 TFLOP/s (0.28 ms for eight chunks of 1 to 1024 tokens on up to
+// e4m3 caches reach 590 TFLOP/s (0.27 ms for eight chunks of 1 to 1024 tokens on up to
 // 4096; runs of 64 0.33 ms, of 32 0.41): MFMA busy 24 %, VALU 35 %, the rest is the wait
 // for a block's codes between its loads and its conversion. Page numbers looked up a
-// block ahead did not shorten it (0.30 ms). Heads of 256 reach 385 TFLOP/s: 128
+// block ahead did not shorten it (0.30 ms). Heads of 256 reach 438 TFLOP/s: 128
 // accumulators and 64 query registers leave one wave per SIMD, and nothing covers
 // its LDS latencies (a ring of four blocks: 324 -> 355 us).
 //
@@ -310,7 +310,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 
         // Two workgroups share a CU (bf16, heads up to 128): the one at its MFMAs goes first, so
         // that the other's softmax fills in behind it instead of beside it (prompt of 8192:
-        // 588 -> 559 us; with e4m3's longer softmax, or one workgroup per CU, it costs 1 to 6 %).
+        // 589 -> 569 us; with e4m3's longer softmax, or one workgroup per CU, it costs 1 to 6 %).
         constexpr bool FIRST = !FP8 && DP <= 128;
         if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         // scores: register i of block nb holds position k0 + 32 nb + 8 (i / 4) + 4 half + i % 4
