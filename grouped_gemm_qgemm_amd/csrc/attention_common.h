@@ -136,11 +136,11 @@ __device__ __forceinline__ int attn_chunk(const AttnArgs& p, unsigned long long 
 }
 __device__ __forceinline__ int attn_chunks(int span, int chunk) { return span <= chunk ? 1 : (span + chunk - 1) / chunk; }
 
-// Item `want` of the launch, for head h; all NT threads call it. Items are ordered
+// Item `want` of each head; all NT threads call it. Items are ordered
 // by sequence, then chunk, then tile (the last tiles, which see the most positions,
 // first). Workgroup 0 also writes the workspace's count of records.
 template <int NT>
-__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, int h, AttnScan<NT>& sh) {
+__device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (p.batch <= 64) {
     // every wave looks at all sequences, one per lane: no barrier. The longest sequences

@@ -4,9 +4,9 @@
 //   s_i = scale * sum_d q[d] * k_i[d]          over the positions i a row sees
 //   out = sum_i e^(s_i - m) v_i / sum_i e^(s_i - m)
 //
-// The rows of a tile are 128 * RT consecutive (token, query head) pairs of one
+// The rows of a tile are 128 consecutive (token, query head) pairs of one
 // key/value head, token-major, so its pages are read once for all query heads
-// that share them. Each of four waves owns 32 * RT rows and computes the scores
+// that share them. Each of four waves owns 32 rows and computes the scores
 // transposed, S^T = K Q^T with 32x32x16 MFMAs: a lane then holds scores of one
 // row only, the running maximum and sum need one exchange with the other half of
 // the wave, and the probabilities are already the B operand of O^T = V^T P^T (the
@@ -75,7 +75,7 @@ struct AttnTileLds {
 // One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
 // values are selected per token. Without it, returns whether some output came out
 // as an infinity or NaN, for the whole workgroup, and then has written nothing.
-template <int DP, int GRAN, int RT, bool SAFE>
+template <int DP, int GRAN, bool SAFE>
 __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int NT = AW * 64;
@@ -109,25 +109,18 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   }
 
   const int rows = it.fresh * p.group;
-  int tok[RT], hi[RT], lo[RT];
-  u32x4_t qf[RT][NS];
+  const int my_row = min(t.r_first + wave * 32 + col, rows - 1), tok = over_group(p, my_row);
+  const int hi = p.causal ? it.cached + tok : it.cached + it.fresh - 1;
+  const int lo = p.window ? it.cached + tok - p.window + 1 : 0;
+  const uint16_t* q = p.q + ((size_t)(it.row0 + tok) * p.hq + h * p.group + my_row - tok * p.group) * p.d;
+  u32x4_t qf[NS];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int r = min(t.r_first + (wave * RT + rt) * 32 + col, rows - 1);
-    tok[rt] = over_group(p, r);
-    hi[rt] = p.causal ? it.cached + tok[rt] : it.cached + it.fresh - 1;
-    lo[rt] = p.window ? it.cached + tok[rt] - p.window + 1 : 0;
-    const uint16_t* q = p.q + ((size_t)(it.row0 + tok[rt]) * p.hq + h * p.group + r - tok[rt] * p.group) * p.d;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int d = 16 * s + 8 * half;
-      qf[rt][s] = d < p.d ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
-    }
+  for (int s = 0; s < NS; ++s) {
+    const int d = 16 * s + 8 * half;
+    qf[s] = d < p.d ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
   }
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int s = 0; s < NS; ++s) arrived(qf[rt][s]);
+  for (int s = 0; s < NS; ++s) arrived(qf[s]);
   const float cs = p.scale * kLog2e;
   const int runs = FP8 ? p.d / (FP8 ? GRAN : 1) : 1;
   const int chunks = p.d / 8;                                 // chunks of an LDS row that exist
@@ -154,18 +147,13 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     voff[k] = (key & 15) * (uint32_t)row_bytes + c;
   }
 
-  float16_t acc[RT][ND];
-  float m[RT], l[RT];     // reference of the weights' exponents (base 2), this lane's share of their sum
+  float16_t acc[ND];
+  float m = -INFINITY, l = 0.f;   // reference of the weights' exponents (base 2), this lane's share of their sum
   {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      m[rt] = -INFINITY;
-      l[rt] = 0.f;
+    for (int n = 0; n < ND; ++n)
 #pragma unroll
-      for (int n = 0; n < ND; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[rt][n][i] = 0.f;
-    }
+      for (int i = 0; i < 16; ++i) acc[n][i] = 0.f;
     // as many positions at a time as the list of pages covers
     const int seg = by16 ? it.chunk : (int)min((long long)it.chunk, (long long)(TPG - 1) * p.page_size / KB * KB);
     for (int s_first = c_first; s_first < c_end; s_first += seg) {
@@ -279,7 +267,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             uint32_t o[8];
 #pragma unroll
             for (int g = 0; g < 4; ++g) e4m3x4_to_bf16(stage[plane][k][g], o[2 * g], o[2 * g + 1]);
-            const int z = plane ? swz_t<DP>(key) : swz_t<DP>(key);
+            const int z = swz_t<DP>(key);
             ring[at][plane][key * CH + ((2 * c) ^ z)] = u32x4_t{o[0], o[1], o[2], o[3]};
             ring[at][plane][key * CH + ((2 * c + 1) ^ z)] = u32x4_t{o[4], o[5], o[6], o[7]};
           }
@@ -314,20 +302,17 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         constexpr bool FIRST = !FP8 && DP <= 128;
         if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         // scores: register i of block nb holds position k0 + 32 nb + 8 (i / 4) + 4 half + i % 4
-        float16_t sc[RT][NB];
+        float16_t sc[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const int key = nb * 32 + col;
-          float16_t part[RT];
+          float16_t part;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[rt][e] = 0.f;
+          for (int e = 0; e < 16; ++e) part[e] = 0.f;
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
             const u32x4_t kf = lk[key * CH + ((2 * s + half) ^ swz_t<DP>(key))];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) part[rt] = mfma32x32x16_bf16(kf, qf[rt][s], part[rt]);
+            part = mfma32x32x16_bf16(kf, qf[s], part);
             if constexpr (FP8) {
               if ((s + 1) % RS == 0) {   // a run is complete: times the keys' scales
                 const int run = (s + 1) / RS - 1;
@@ -335,13 +320,11 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
                 for (int g = 0; g < 4; ++g) {
                   const float4_t ks = *reinterpret_cast<const float4_t*>(&ring_s[at][0][run][nb * 32 + 8 * g + 4 * half]);
 #pragma unroll
-                  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                      sc[rt][nb][4 * g + e] = run == 0 ? part[rt][4 * g + e] * ks[e]
-                                                       : __builtin_fmaf(part[rt][4 * g + e], ks[e], sc[rt][nb][4 * g + e]);
-                      part[rt][4 * g + e] = 0.f;
-                    }
+                  for (int e = 0; e < 4; ++e) {
+                    sc[nb][4 * g + e] =
+                        run == 0 ? part[4 * g + e] * ks[e] : __builtin_fmaf(part[4 * g + e], ks[e], sc[nb][4 * g + e]);
+                    part[4 * g + e] = 0.f;
+                  }
                 }
                 // Runs of one or two pairs of MFMAs: finished before the next run begins. Left
                 // alone, the compiler keeps a set of partial scores per run and spills (eight
@@ -349,71 +332,60 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
                 // heads of 256: 4.36 -> 1.30, 1.44 -> 1.10). Runs of 128 have room for two
                 // (heads of 256: 0.88 ms, and 0.95 in turn).
                 if constexpr (R > 1 && GRAN < 128) {
-#pragma unroll
-                  for (int rt = 0; rt < RT; ++rt) asm volatile("" : "+v"(sc[rt][nb]));
+                  asm volatile("" : "+v"(sc[nb]));
                   __builtin_amdgcn_sched_barrier(0);
                 }
               }
             }
           }
-          if constexpr (!FP8) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) sc[rt][nb] = part[rt];
-          }
+          if constexpr (!FP8) sc[nb] = part;
         }
         if constexpr (FIRST) __builtin_amdgcn_s_setprio(0);
         const bool masked = uniform((p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
                                     k0 + KB > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end));
         if (masked) {
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            // positions lo .. min(hi, s_end - 1), counted from lo
-            const uint32_t seen = max(min(hi[rt], s_end - 1) - lo[rt] + 1, 0), first = k0 + 4 * half - lo[rt];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                sc[rt][nb][e] = first + (nb * 32 + 8 * (e / 4) + e % 4) < seen ? sc[rt][nb][e] : -INFINITY;
-          }
-        }
-        float base[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          float mx = -INFINITY;
+          // positions lo .. min(hi, s_end - 1), counted from lo
+          const uint32_t seen = max(min(hi, s_end - 1) - lo + 1, 0), first = k0 + 4 * half - lo;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[rt][nb][e]);
-          mx = max_halves(mx) * cs;
-          if (__any(mx > m[rt] + kSlack || (m[rt] == -INFINITY && mx > -INFINITY))) {
-            const float top = fmaxf(m[rt], mx);
-            const float alpha = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[rt] - top);
-            m[rt] = top;
-            l[rt] *= alpha;
-#pragma unroll
-            for (int n = 0; n < ND; ++n)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) acc[rt][n][e] *= alpha;
-          }
-          // a row that has seen nothing yet keeps -infinity; its weights are 0
-          base[rt] = m[rt] == -INFINITY ? 0.f : m[rt];
-          float sum = 0.f;
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              sc[rt][nb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[rt][nb][e], cs, -base[rt]));
-              sum += sc[rt][nb][e];
-            }
-          l[rt] += sum;
+            for (int e = 0; e < 16; ++e)
+              sc[nb][e] = first + (nb * 32 + 8 * (e / 4) + e % 4) < seen ? sc[nb][e] : -INFINITY;
         }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[nb][e]);
+        mx = max_halves(mx) * cs;
+        if (__any(mx > m + kSlack || (m == -INFINITY && mx > -INFINITY))) {
+          const float top = fmaxf(m, mx);
+          const float alpha = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+          m = top;
+          l *= alpha;
+#pragma unroll
+          for (int n = 0; n < ND; ++n)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[n][e] *= alpha;
+        }
+        // a row that has seen nothing yet keeps -infinity; its weights are 0
+        const float base = m == -INFINITY ? 0.f : m;
+        float sum = 0.f;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            sc[nb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nb][e], cs, -base));
+            sum += sc[nb][e];
+          }
+        l += sum;
 
         // weights of 16 positions as the B operand; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
-        auto weights = [&](int rt, int nb, int ks, int run) {
+        auto weights = [&](int nb, int ks, int run) {
           float w[8];
           const int key0 = nb * 32 + ks * 16 + 4 * half;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = sc[rt][nb][8 * ks + e];
+          for (int e = 0; e < 8; ++e) w[e] = sc[nb][8 * ks + e];
           if constexpr (FP8) {   // times the value scales of the strip's run
             const float4_t v0 = *reinterpret_cast<const float4_t*>(&ring_s[at][1][run][key0]);
             const float4_t v1 = *reinterpret_cast<const float4_t*>(&ring_s[at][1][run][key0 + 8]);
@@ -426,7 +398,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int pos = k0 + key0 + e % 4 + 8 * (e / 4);
-                if (pos > hi[rt] || pos < lo[rt] || pos >= s_end) w[e] = 0.f;
+                if (pos > hi || pos < lo || pos >= s_end) w[e] = 0.f;
               }
             }
           }
@@ -447,16 +419,12 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              u32x4_t pf[RT];
+              u32x4_t pf;
 #pragma unroll
               for (int n = 0; n < ND; ++n) {
-                if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) {
-#pragma unroll
-                  for (int rt = 0; rt < RT; ++rt) pf[rt] = weights(rt, nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
-                }
+                if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
                 const u32x4_t vf = values(nb, ks, n);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) acc[rt][n] = mfma32x32x16_bf16(vf, pf[rt], acc[rt][n]);
+                acc[n] = mfma32x32x16_bf16(vf, pf, acc[n]);
               }
             }
         } else {
@@ -468,25 +436,22 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
               for (int n = 0; n < ND; ++n) {
                 const u32x4_t vf = values(nb, ks, n);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                  const u32x4_t pf = weights(rt, nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
+                const u32x4_t pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
 #pragma unroll 1
-                  for (int tt = t.t_first; tt <= t.t_last; ++tt) {
-                    const int t_hi = p.causal ? it.cached + tt : it.cached + it.fresh - 1;
-                    const int t_lo = p.window ? it.cached + tt - p.window + 1 : 0;
-                    uint32_t keep[8];
+                for (int tt = t.t_first; tt <= t.t_last; ++tt) {
+                  const int t_hi = p.causal ? it.cached + tt : it.cached + it.fresh - 1;
+                  const int t_lo = p.window ? it.cached + tt - p.window + 1 : 0;
+                  uint32_t keep[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                      const int pos = k0 + nb * 32 + ks * 16 + 4 * half + e % 4 + 8 * (e / 4);
-                      keep[e] = pos <= t_hi && pos >= t_lo && pos < s_end ? 0xFFFFu : 0u;
-                    }
-                    const u32x4_t vs = {vf.x & (keep[0] | keep[1] << 16), vf.y & (keep[2] | keep[3] << 16),
-                                        vf.z & (keep[4] | keep[5] << 16), vf.w & (keep[6] | keep[7] << 16)};
-                    const float16_t with = mfma32x32x16_bf16(vs, pf, acc[rt][n]);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[rt][n][e] = tt == tok[rt] ? with[e] : acc[rt][n][e];
+                  for (int e = 0; e < 8; ++e) {
+                    const int pos = k0 + nb * 32 + ks * 16 + 4 * half + e % 4 + 8 * (e / 4);
+                    keep[e] = pos <= t_hi && pos >= t_lo && pos < s_end ? 0xFFFFu : 0u;
                   }
+                  const u32x4_t vs = {vf.x & (keep[0] | keep[1] << 16), vf.y & (keep[2] | keep[3] << 16),
+                                      vf.z & (keep[4] | keep[5] << 16), vf.w & (keep[6] | keep[7] << 16)};
+                  const float16_t with = mfma32x32x16_bf16(vs, pf, acc[n]);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) acc[n][e] = tt == tok ? with[e] : acc[n][e];
                 }
               }
         }
@@ -498,11 +463,9 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     }
     int off = 0;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int n = 0; n < ND; ++n)
 #pragma unroll
-      for (int n = 0; n < ND; ++n)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[rt][n][e]) < INFINITY);
+      for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[n][e]) < INFINITY);
     if (!SAFE) {
       off = __any(off);
       if (lane == 0) lds.w_off[wave] = off;
@@ -516,59 +479,56 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
   float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(p.bm, DP);
+  const float sum = l + __shfl_xor(l, 32);
+  const int r = wave * 32 + col;
+  if (r >= t.r_count) return false;
+  if (alone) {
+    const float inv = 1.f / sum;   // every row sees a position
+    const int row = t.r_first + r, token = over_group(p, row);
+    uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const float sum = l[rt] + __shfl_xor(l[rt], 32);
-    const int r = (wave * RT + rt) * 32 + col;
-    if (r >= t.r_count) continue;
-    if (alone) {
-      const float inv = 1.f / sum;   // every row sees a position
-      const int row = t.r_first + r, token = over_group(p, row);
-      uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
+    for (int n = 0; n < ND; ++n)
 #pragma unroll
-      for (int n = 0; n < ND; ++n)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int d = n * 32 + 8 * g + 4 * half;
-          if (d < p.d)
-            *reinterpret_cast<u32x2_t*>(to + d) = u32x2_t{f2bf2_rn(acc[rt][n][4 * g] * inv, acc[rt][n][4 * g + 1] * inv),
-                                                          f2bf2_rn(acc[rt][n][4 * g + 2] * inv, acc[rt][n][4 * g + 3] * inv)};
-        }
-    } else {
-#pragma unroll
-      for (int n = 0; n < ND; ++n)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + n * 32 + 8 * g + 4 * half) =
-              float4_t{acc[rt][n][4 * g], acc[rt][n][4 * g + 1], acc[rt][n][4 * g + 2], acc[rt][n][4 * g + 3]};
-      if (half == 0) {
-        ws[(size_t)p.bm * DP + 2 * r] = m[rt];
-        ws[(size_t)p.bm * DP + 2 * r + 1] = sum;
+      for (int g = 0; g < 4; ++g) {
+        const int d = n * 32 + 8 * g + 4 * half;
+        if (d < p.d)
+          *reinterpret_cast<u32x2_t*>(to + d) = u32x2_t{f2bf2_rn(acc[n][4 * g] * inv, acc[n][4 * g + 1] * inv),
+                                                        f2bf2_rn(acc[n][4 * g + 2] * inv, acc[n][4 * g + 3] * inv)};
       }
+  } else {
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + n * 32 + 8 * g + 4 * half) =
+            float4_t{acc[n][4 * g], acc[n][4 * g + 1], acc[n][4 * g + 2], acc[n][4 * g + 3]};
+    if (half == 0) {
+      ws[(size_t)p.bm * DP + 2 * r] = m;
+      ws[(size_t)p.bm * DP + 2 * r + 1] = sum;
     }
   }
   return false;
 }
 
 // Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
-template <int DP, int GRAN, int RT>
+template <int DP, int GRAN>
 __device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_tile<DP, GRAN, RT, true>(p, uniform(it), blockIdx.x % p.hkv, *lds);
+  attend_tile<DP, GRAN, true>(p, uniform(it), blockIdx.x % p.hkv, *lds);
 }
 
-template <int DP, int GRAN, int RT>
+template <int DP, int GRAN>
 __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
   __shared__ AttnTileLds<DP, GRAN> lds;
   const int h = blockIdx.x % p.hkv;
-  const AttnItem it = attn_locate<AW * 64>(p, blockIdx.x / p.hkv, h, lds.scan);
+  const AttnItem it = attn_locate<AW * 64>(p, blockIdx.x / p.hkv, lds.scan);
   if (it.b < 0) return;
-  if (attend_tile<DP, GRAN, RT, false>(p, it, h, lds))
-    attend_tile_safe<DP, GRAN, RT>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
+  if (attend_tile<DP, GRAN, false>(p, it, h, lds))
+    attend_tile_safe<DP, GRAN>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
 }
 
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream) {
-#define QG_ATTN(DP, GRAN) attention_tile_kernel<DP, GRAN, 1><<<grid, AW * 64, 0, stream>>>(p)
+#define QG_ATTN(DP, GRAN) attention_tile_kernel<DP, GRAN><<<grid, AW * 64, 0, stream>>>(p)
   const int gran = p.fp8 ? p.gran : 0;
   if (p.d <= 64) {
     if (gran == 0) QG_ATTN(64, 0);
