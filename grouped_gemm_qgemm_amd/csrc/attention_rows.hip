@@ -54,6 +54,19 @@ struct AttnRowsLds {
   ShareScan<NW * 64> scan;
 };
 
+// Eight bf16 with zero in place of infinities and NaN, for their product with the
+// remainders of probabilities: a remainder is zero or of either sign, so an infinite
+// value times one would be NaN where the value times the probability is infinite.
+__device__ __forceinline__ u32x4_t finite(u32x4_t v) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = v[i];
+    r[i] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+  }
+  return r;
+}
+
 }  // namespace
 
 // Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1
@@ -317,6 +330,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       }
       u32x4_t pf[MT][2];    // probabilities: value and remainder
       auto split_p = [&](int mt, int run) {
+#pragma clang fp contract(off)   // the same remainder whatever the code around it: not one of an unrounded product
         uint32_t a[4], b[4];
         float4_t vs[2];
         if constexpr (FP8) {   // times the value scales of the strip's run
@@ -337,7 +351,13 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
             }
           }
           a[g] = f2bf2_rn(x[0], x[1]);
-          b[g] = f2bf2_rn(x[0] - bf2f((uint16_t)a[g]), x[1] - bf2f((uint16_t)(a[g] >> 16)));
+          float rest[2] = {x[0] - bf2f((uint16_t)a[g]), x[1] - bf2f((uint16_t)(a[g] >> 16))};
+          if (FP8 && SAFE) {   // an infinite scale has no remainder
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              if (!(fabsf(rest[u]) < INFINITY)) rest[u] = 0.f;
+          }
+          b[g] = f2bf2_rn(rest[0], rest[1]);
         }
         pf[mt][0] = u32x4_t{a[0], a[1], a[2], a[3]};
         pf[mt][1] = u32x4_t{b[0], b[1], b[2], b[3]};
@@ -370,8 +390,8 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
             acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][0], acc[mt][n]);
             acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][1], acc[mt][n]);
           } else if (!masked) {
-            // without the remainder: times an infinite value it would be NaN
             acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][0], acc[mt][n]);
+            acc[mt][n] = mfma16x16x32_bf16(finite(vf), pf[mt][1], acc[mt][n]);
           } else {
             // token by token, with the values it does not see set to zero
 #pragma unroll 1
@@ -387,7 +407,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
               const uint32_t v0 = vf.x, v1 = vf.y, v2 = vf.z, v3 = vf.w;
               const u32x4_t vs = {v0 & (keep[0] | keep[1] << 16), v1 & (keep[2] | keep[3] << 16),
                                   v2 & (keep[4] | keep[5] << 16), v3 & (keep[6] | keep[7] << 16)};
-              const float4_t with = mfma16x16x32_bf16(vs, pf[mt][0], acc[mt][n]);
+              const float4_t with = mfma16x16x32_bf16(finite(vs), pf[mt][1], mfma16x16x32_bf16(vs, pf[mt][0], acc[mt][n]));
               if (tt == tok[mt]) acc[mt][n] = with;
             }
           }

@@ -1,0 +1,80 @@
+"""attention_ragged_paged where numbers are extreme: what a row does not see must not change a
+bit of it."""
+import numpy as np
+import pytest
+import torch
+
+import synth
+from attention_shapes import kernel, tile_cuts
+from gpu_util import bf16v, say
+from test_gpu_attention import _drafts, compare, exact, run
+
+pytestmark = pytest.mark.gpu
+
+
+def cus():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def history(batch, first):
+    return [first] + [5 + 2 * i for i in range(batch - 1)]
+
+
+# name: new tokens, history, query heads, key/value heads; sequence 0 is the one looked at
+FORMS = {
+    "rows1": ([4, 2, 1], [70, 3, 60], 4, 2),
+    "rows1 cut": ([4, 2, 1], [3000, 3, 60], 4, 2),
+    "rows2": (_drafts(34, 40, 4), history(34, 70), 8, 2),
+    "rows2 cut": (_drafts(34, 40, 4), history(34, 3000), 8, 2),
+    "tile": ([150, 2, 1], [70, 3, 60], 4, 2),
+    "tile cut": ([150, 2, 1], [3000, 3, 60], 4, 2),
+}
+
+
+def case(seed, form, dim, gran):
+    new, hist, hq, hkv = FORMS[form]
+    d = synth.attention_inputs(seed, new, hist, hq=hq, hkv=hkv, d=dim, gran=gran)
+    assert kernel(d, cus()) == form.split()[0]
+    if form == "tile cut":
+        assert tile_cuts(d)[1][0] > 1
+    say(f"[extremes] {form} q {d.q.shape} head {dim} gran {gran}")
+    return d
+
+
+def put(d, plane, pos, value):
+    """One element of every head at one position of sequence 0."""
+    page, slot = d.page_table[0, pos // 16], pos % 16
+    if not d.gran:
+        d.blocks[d.layer_idx, plane, page, slot, :, 5] = synth.bf16_bits(np.array([value]))[0]
+    elif np.isnan(value):
+        d.blocks[d.layer_idx, plane, page, slot, :, 5] = 0x7F
+    else:
+        d.scales[d.layer_idx, plane, page, slot, :, 0] = value
+
+
+def blind(d, at, window):
+    """Rows that do not see position `at` of sequence 0."""
+    rows = np.ones(len(d.q), bool)
+    first = at - int(d.cache_lengths[0])
+    new = int(d.row_offsets[1])
+    rows[first:min(new, first + window) if window else new] = False
+    return rows
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dim,gran", [(64, 0), (64, 32), (128, 128), (256, 0), (256, 64)])
+@pytest.mark.parametrize("window", [0, 2])
+def test_a_value_that_a_row_does_not_see_changes_no_bit_of_it(lib, gpu, form, dim, gran, window):
+    """Infinities and NaN in one position's values, or in their scales."""
+    if form.startswith("rows2") and window:
+        window = 20   # (its first sequence has 40 new tokens)
+    d = case(50, form, dim, gran)
+    at = int(d.cache_lengths[0]) + (2 if form.startswith("rows1") else 17)
+    clean = run(lib, d, 0.125, True, window)
+    hidden = blind(d, at, window)
+    for value in (float("nan"), float("inf")):
+        put(d, 1, at, value)
+        got = run(lib, d, 0.125, True, window)
+        assert not np.isfinite(bf16v(got)[~hidden]).all()
+        compare(d, got, exact(d, 0.125, True, window), form)
+        assert np.array_equal(got[hidden], clean[hidden]), f"{int((got != clean)[hidden].sum())} elements changed by {value}"
