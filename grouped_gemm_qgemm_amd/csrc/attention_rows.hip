@@ -309,10 +309,11 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx = fmaxf(mx, sc[mt][e >> 2][e & 3]);
         mx = max_halves(max_quarters(mx)) * cs;
-        if (__any(mx > m[mt] + kSlack || (m[mt] == -INFINITY && mx > -INFINITY))) {
-          const float top = fmaxf(m[mt], mx);
-          const float alpha = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[mt] - top);
-          m[mt] = top;
+        const bool more = mx > m[mt] + kSlack;   // (-infinity: the row has seen nothing yet)
+        if (__any(more)) {
+          // only a row's own scores move its reference: its result is the same whatever the others see
+          const float alpha = more ? __builtin_amdgcn_exp2f(m[mt] - mx) : 1.f;
+          m[mt] = more ? mx : m[mt];
           l[mt] *= alpha;
 #pragma unroll
           for (int n = 0; n < ND; ++n) acc[mt][n] *= alpha;

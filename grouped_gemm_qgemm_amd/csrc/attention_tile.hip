@@ -358,10 +358,11 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
           for (int e = 0; e < 16; ++e) mx = fmaxf(mx, sc[nb][e]);
         mx = max_halves(mx) * cs;
-        if (__any(mx > m + kSlack || (m == -INFINITY && mx > -INFINITY))) {
-          const float top = fmaxf(m, mx);
-          const float alpha = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
-          m = top;
+        const bool more = mx > m + kSlack;   // (-infinity: the row has seen nothing yet)
+        if (__any(more)) {
+          // only a row's own scores move its reference: its result is the same whatever the others see
+          const float alpha = more ? __builtin_amdgcn_exp2f(m - mx) : 1.f;
+          m = more ? mx : m;
           l *= alpha;
 #pragma unroll
           for (int n = 0; n < ND; ++n)

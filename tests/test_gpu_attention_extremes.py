@@ -78,3 +78,30 @@ def test_a_value_that_a_row_does_not_see_changes_no_bit_of_it(lib, gpu, form, di
         assert not np.isfinite(bf16v(got)[~hidden]).all()
         compare(d, got, exact(d, 0.125, True, window), form)
         assert np.array_equal(got[hidden], clean[hidden]), f"{int((got != clean)[hidden].sum())} elements changed by {value}"
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dim,gran", [(64, 0), (64, 32), (128, 128), (256, 0), (256, 64)])
+@pytest.mark.parametrize("window", [0, 2])
+def test_a_key_that_a_row_does_not_see_changes_no_bit_of_it(lib, gpu, form, dim, gran, window):
+    """One position's keys are such that the rows which see it get the largest of their scores
+    there, an infinite one, or NaN; the rows that do not share their waves with those."""
+    if form.startswith("rows2") and window:
+        window = 20
+    d = case(51, form, dim, gran)
+    at = int(d.cache_lengths[0]) + (2 if form.startswith("rows1") else 17)
+    clean = run(lib, d, 0.125, True, window)
+    hidden = blind(d, at, window)
+    page, slot = d.page_table[0, at // 16], at % 16
+    for value in (float("nan"), float("inf"), None):
+        if value is None:
+            # eight times the length of the others, and so of its scores
+            if gran:
+                d.blocks[1, 0, page, slot] = 0x70
+                d.scales[1, 0, page, slot] = 0.0625
+            else:
+                d.blocks[1, 0, page, slot] = synth.bf16_bits(np.random.default_rng(3).standard_normal((d.blocks.shape[4], dim)) * 8)
+        else:
+            put(d, 0, at, value)
+        got = run(lib, d, 0.125, True, window)
+        assert np.array_equal(got[hidden], clean[hidden]), f"{int((got != clean)[hidden].sum())} elements changed by {value}"
