@@ -35,6 +35,26 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWideBlocks = 8;   // (see attn_share)
 constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row's reference
 
+// Sums of values by weights of up to 2^8 may leave fp32's range where their mean, the
+// result, does not. One pass is enough for accumulators below 2^116: those of four waves
+// and 512 parts can be added without a thought. A row with larger ones is computed
+// again (by the pass that selects values), its weights divided by a power of two that makes
+// their sum over all positions at most 1/4, so that the sums, those of the other parts
+// included, stay in range; the reference that goes with them says so.
+constexpr float kSumsMost = 0x1p116f;
+constexpr int kRepeats = 2;   // runs of the pass that selects values: a row changes once
+struct AttnRepeat {
+  int shift = 0;              // log2 of what the row's weights are divided by
+  __device__ __forceinline__ float weight(float w) const { return __builtin_amdgcn_ldexpf(w, -shift); }
+  __device__ __forceinline__ float reference(float m) const { return m + (float)shift; }
+  // large: some accumulator is not below kSumsMost. Whether the row has to be computed again.
+  __device__ __forceinline__ bool again(bool large, int positions) {
+    if (!large || shift) return false;
+    shift = 42 - __builtin_clz(positions);   // weights are 2^8 at most
+    return true;
+  }
+};
+
 // What one workgroup works on.
 struct AttnItem {
   int b;            // sequence, -1 past the last item

@@ -71,11 +71,13 @@ __device__ __forceinline__ u32x4_t finite(u32x4_t v) {
 
 // Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1
 // and go to that slot of the workspace else. GRAN: head-dim elements per scale of an
-// e4m3 cache, 0 for bf16. SAFE: values are selected per token. Without it, returns whether some output came out
-// as an infinity or NaN, for the whole workgroup, and then has written nothing.
+// e4m3 cache, 0 for bf16. SAFE: values are selected per token. Returns whether some
+// row has to be computed again (without SAFE: some accumulator is too large, an infinity
+// or NaN; with it: as `rep`, the state of this lane's rows in this wave, says), for the
+// whole workgroup, and then has written nothing.
 template <int DP, int GRAN, int MT, int NW, int NST, bool SAFE>
 __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h0, int hw, int c_first, int c_end, int slot,
-                                            AttnRowsLds<DP, GRAN, MT, NW, NST>& lds) {
+                                            AttnRowsLds<DP, GRAN, MT, NW, NST>& lds, AttnRepeat (&rep)[MT]) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int ES = FP8 ? 1 : 2;              // bytes per cached element
   constexpr int CH = DP * ES / 16;             // chunks per LDS row
@@ -323,7 +325,8 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][e >> 2][e & 3], cs, -base));
+          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][e >> 2][e & 3], cs, -base));
+          if (SAFE) x = rep[mt].weight(x);
           sc[mt][e >> 2][e & 3] = x;
           sum += x;
         }
@@ -417,16 +420,23 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     }
   }
   int off = 0;
-  if (!SAFE) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+  for (int mt = 0; mt < MT; ++mt) {
+    int far = 0;
 #pragma unroll
-      for (int n = 0; n < ND; ++n)
+    for (int n = 0; n < ND; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) off |= !(fabsf(acc[mt][n][i]) < INFINITY);
-    off = __any(off);
-    if (lane == 0) lds.w_off[wave] = off;
+      for (int i = 0; i < 4; ++i) far |= !(fabsf(acc[mt][n][i]) < kSumsMost);
+    if (SAFE) {
+      far |= __shfl_xor(far, 16);
+      far |= __shfl_xor(far, 32);
+      m[mt] = rep[mt].reference(m[mt]);
+      far = rep[mt].again(far, t.end - t.start);
+    }
+    off |= far;
   }
+  off = __any(off);
+  if (lane == 0) lds.w_off[wave] = off;
 
   // the waves' results joined through LDS (their rings, which no load targets any more)
   float* mine = reinterpret_cast<float*>(&ring[wave][0][0][0]);
@@ -442,14 +452,12 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n) *reinterpret_cast<float4_t*>(mine + (16 * mt + col) * OS + 16 * n + 4 * j) = acc[mt][n];
   }
   __syncthreads();
-  if (!SAFE) {
-    off = 0;
+  off = 0;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) off |= lds.w_off[w];
-    if (off) {
-      __syncthreads();   // before the rings are used again
-      return true;
-    }
+  for (int w = 0; w < NW; ++w) off |= lds.w_off[w];
+  if (off) {
+    __syncthreads();   // before the rings are used again
+    return true;
   }
   for (int e = tid; e < hw * t.r_count * (DP / 4); e += NT) {
     const int sub = e / (t.r_count * (DP / 4)), r = e / (DP / 4) % t.r_count, d = e % (DP / 4) * 4;
@@ -489,9 +497,12 @@ template <int DP, int GRAN, int MT, int NW, int NST>
 __device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int h, int hw, int c_first, int c_end,
                                                            int slot, AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(hw),
-                                           __builtin_amdgcn_readfirstlane(c_first),
-                                           __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds);
+  AttnRepeat rep[MT];
+  for (int pass = 0; pass < kRepeats; ++pass)
+    if (!attend_rows<DP, GRAN, MT, NW, NST, true>(p, uniform(it), __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(hw),
+                                                  __builtin_amdgcn_readfirstlane(c_first), __builtin_amdgcn_readfirstlane(c_end),
+                                                  __builtin_amdgcn_readfirstlane(slot), *lds, rep))
+      return;
 }
 
 template <int DP, int GRAN, int MT, int NW, int NST>
@@ -525,7 +536,8 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
                                             2 * s.w * p.hkv, 2 * p.hkv, 1};
         }
       }
-      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, s.h, s.hw, c_first, c_end, slot, lds))
+      AttnRepeat none[MT];
+      if (attend_rows<DP, GRAN, MT, NW, NST, false>(p, it, s.h, s.hw, c_first, c_end, slot, lds, none))
         attend_rows_safe<DP, GRAN, MT, NW, NST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, s.hw, c_first, c_end, slot, &lds);
     }
     s.at += take;

@@ -39,8 +39,9 @@
 //
 // A position that a row must not see takes a score of -infinity by selection.
 // Its value row is still multiplied, by zero: where it holds an infinity or NaN
-// the row's output would turn NaN. So a tile whose result is not finite is
-// computed again with the values selected per token.
+// the row's output would turn NaN. So a tile whose accumulators are not finite, or so
+// large that sums of them may not be, is computed again with the values selected per
+// token (and, where large ones are left, smaller weights: AttnRepeat).
 #include "attention_common.h"
 
 namespace qg {
@@ -73,10 +74,11 @@ struct AttnTileLds {
 };
 
 // One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
-// values are selected per token. Without it, returns whether some output came out
-// as an infinity or NaN, for the whole workgroup, and then has written nothing.
+// values are selected per token. Returns whether some row has to be computed again
+// (without SAFE: some accumulator is too large, an infinity or NaN; with it: as `rep`, the
+// state of this lane's row, says), for the whole workgroup, and then has written nothing.
 template <int DP, int GRAN, bool SAFE>
-__device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds) {
+__device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds, AttnRepeat& rep) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int NT = AW * 64;
   constexpr int KB = AttnTileLds<DP, GRAN>::KB;
@@ -377,6 +379,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             sc[nb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nb][e], cs, -base));
+            if (SAFE) sc[nb][e] = rep.weight(sc[nb][e]);
             sum += sc[nb][e];
           }
         l += sum;
@@ -466,16 +469,15 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
     for (int n = 0; n < ND; ++n)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[n][e]) < INFINITY);
-    if (!SAFE) {
-      off = __any(off);
-      if (lane == 0) lds.w_off[wave] = off;
-      __syncthreads();
-      off = 0;
+      for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[n][e]) < kSumsMost);
+    if (SAFE) off = rep.again(off | __shfl_xor(off, 32), t.end - t.start);
+    off = __any(off);
+    if (lane == 0) lds.w_off[wave] = off;
+    __syncthreads();
+    off = 0;
 #pragma unroll
-      for (int w = 0; w < AW; ++w) off |= lds.w_off[w];
-      if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
-    }
+    for (int w = 0; w < AW; ++w) off |= lds.w_off[w];
+    if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
   }
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
@@ -504,7 +506,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + n * 32 + 8 * g + 4 * half) =
             float4_t{acc[n][4 * g], acc[n][4 * g + 1], acc[n][4 * g + 2], acc[n][4 * g + 3]};
     if (half == 0) {
-      ws[(size_t)p.bm * DP + 2 * r] = m;
+      ws[(size_t)p.bm * DP + 2 * r] = SAFE ? rep.reference(m) : m;
       ws[(size_t)p.bm * DP + 2 * r + 1] = sum;
     }
   }
@@ -515,7 +517,9 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 template <int DP, int GRAN>
 __device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
   const AttnArgs p = reload_args(args);
-  attend_tile<DP, GRAN, true>(p, uniform(it), blockIdx.x % p.hkv, *lds);
+  AttnRepeat rep;
+  for (int pass = 0; pass < kRepeats; ++pass)
+    if (!attend_tile<DP, GRAN, true>(p, uniform(it), blockIdx.x % p.hkv, *lds, rep)) return;
 }
 
 template <int DP, int GRAN>
@@ -524,7 +528,8 @@ __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kern
   const int h = blockIdx.x % p.hkv;
   const AttnItem it = attn_locate<AW * 64>(p, blockIdx.x / p.hkv, lds.scan);
   if (it.b < 0) return;
-  if (attend_tile<DP, GRAN, false>(p, it, h, lds))
+  AttnRepeat none;
+  if (attend_tile<DP, GRAN, false>(p, it, h, lds, none))
     attend_tile_safe<DP, GRAN>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
 }
 

@@ -1,5 +1,5 @@
 """attention_ragged_paged where numbers are extreme: what a row does not see must not change a
-bit of it."""
+bit of it, and large finite values must give the formula's finite results."""
 import numpy as np
 import pytest
 import torch
@@ -105,3 +105,63 @@ def test_a_key_that_a_row_does_not_see_changes_no_bit_of_it(lib, gpu, form, dim,
             put(d, 0, at, value)
         got = run(lib, d, 0.125, True, window)
         assert np.array_equal(got[hidden], clean[hidden]), f"{int((got != clean)[hidden].sum())} elements changed by {value}"
+
+
+def huge_values(d, growing):
+    """Values of 2^125 to 2^126 in the first 64 dims, about 1 in the others; the sign depends on the
+    head and dim alone, so that the weighted mean is as large. growing: scores that grow along
+    the sequences, so that weights exceed 1 against the reference that rows keep."""
+    rng = np.random.default_rng(7)
+    L, _, P, S, hkv, D = d.blocks.shape
+    sign = np.where(rng.random((hkv, D)) < 0.5, -1.0, 1.0)
+    size = rng.uniform(0.5, 1.0, (P, S, hkv, D))
+    big = np.arange(D) < 64
+    held = (d.blocks[1, 1] != 0xFFFF) if not d.gran else (d.blocks[1, 1] != 0x7F)
+    if d.gran:
+        codes = synth.e4m3_codes(sign * size * 448)
+        d.blocks[1, 1] = np.where(held, codes, 0x7F)
+        runs = np.where(big.reshape(-1, d.gran)[:, 0], 2.0**126, 1.0) / 448
+        d.scales[1, 1] = np.where(np.isnan(d.scales[1, 1]), np.nan, runs).astype(np.float32)
+    else:
+        d.blocks[1, 1] = np.where(held, synth.bf16_bits(sign * size * np.where(big, 2.0**126, 1.0)), 0xFFFF)
+    if growing:
+        for b in range(len(d.cache_lengths)):
+            n = int(d.cache_lengths[b]) + int(d.row_offsets[b + 1]) - int(d.row_offsets[b])
+            at = np.arange(n)
+            k = np.zeros((n, hkv, D))
+            k[:, :, 0] = np.linspace(0.0, 30.0, n)[:, None]
+            if d.gran:
+                d.blocks[1, 0, d.page_table[b, at // S], at % S] = synth.e4m3_codes(k * 8)
+                d.scales[1, 0, d.page_table[b, at // S], at % S] = 0.125
+            else:
+                d.blocks[1, 0, d.page_table[b, at // S], at % S] = synth.bf16_bits(k)
+        d.q[:] = synth.bf16_bits(np.broadcast_to(np.eye(D)[0], d.q.shape))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("gran", [0, 64])
+@pytest.mark.parametrize("growing", [False, True])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_sums_of_large_values_do_not_leave_the_type(lib, gpu, form, gran, growing, dim):
+    """The weighted mean of finite values is finite, however many they are."""
+    d = case(52, form, dim, gran)
+    huge_values(d, growing)
+    scale = 1.0 if growing else 0.125
+    ref = exact(d, scale)
+    assert np.isfinite(ref[0]).all() and np.abs(ref[0]).max() > 2.0**125
+    say(f"[extremes]   worst element at {compare(d, run(lib, d, scale), ref, form):.2f} of its tolerance")
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("gran", [0, 64])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_large_values_beside_an_infinite_one(lib, gpu, form, gran, bad):
+    """Rows that see it and rows that do not, all of which have sums that are too large as they are."""
+    d = case(54, form, 128, gran)
+    huge_values(d, False)
+    clean = run(lib, d, 0.125)
+    at = int(d.cache_lengths[0]) + (2 if form.startswith("rows1") else 17)
+    put(d, 1, at, float(bad))
+    got, hidden = run(lib, d, 0.125), blind(d, at, 0)
+    compare(d, got, exact(d, 0.125), form)
+    assert np.isfinite(bf16v(got)[hidden]).all() and np.array_equal(got[hidden], clean[hidden])
