@@ -520,6 +520,22 @@ __device__ __forceinline__ float max_quarters(float x) {
   return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
 }
 
+// Where some values are infinities or NaN they enter a product of their own, with weights
+// of one where the row sees the position: the result is theirs however small the weight
+// (an infinity times a weight that has vanished would be NaN). finite(v): eight bf16 with
+// zero in place of them.
+__device__ __forceinline__ u32x4_t finite(u32x4_t v) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = v[i];
+    r[i] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
+  }
+  return r;
+}
+// x where it is an infinity or NaN, else x * f
+__device__ __forceinline__ float times(float x, float f) { return fabsf(x) < INFINITY ? x * f : x; }
+
 // eight transposed bf16 rows x 16 columns: see the kernels for the lanes' order
 __device__ __forceinline__ uint64_t lds_read_tr16(const void* p) {
   return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(

@@ -56,39 +56,47 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int part
 #pragma unroll
     for (int k = 32; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
     const float base = top == -INFINITY ? 0.f : top;
-    float4_t o = {0.f, 0.f, 0.f, 0.f};
-    float sum = 0.f;
-    auto add = [&](auto steps, int s0) {   // parts s0, s0 + PH, ..: `steps` of them
-      constexpr int U = decltype(steps)::value;
-      float4_t x[U];
-      float2_t m[U];
+    float4_t o;
+    float sum;
+    // KEEP: infinities and NaN stay, however small the part's share
+    auto join = [&](auto keep) {
+      constexpr bool KEEP = decltype(keep)::value;
+      o = float4_t{0.f, 0.f, 0.f, 0.f};
+      sum = 0.f;
+      auto add = [&](auto steps, int s0) {   // parts s0, s0 + PH, ..: `steps` of them
+        constexpr int U = decltype(steps)::value;
+        float4_t x[U];
+        float2_t m[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float* from = part_at(min(s0 + u * PH, ns - 1));
-        x[u] = *reinterpret_cast<const float4_t*>(from + (size_t)r * DP + d);
-        m[u] = *reinterpret_cast<const float2_t*>(from + ml);
+        for (int u = 0; u < U; ++u) {
+          const float* from = part_at(min(s0 + u * PH, ns - 1));
+          x[u] = *reinterpret_cast<const float4_t*>(from + (size_t)r * DP + d);
+          m[u] = *reinterpret_cast<const float2_t*>(from + ml);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float f = __builtin_amdgcn_exp2f(m[u].x - base);
+          if (s0 + u * PH < ns) {
+            sum = __builtin_fmaf(m[u].y, f, sum);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i], KEEP && !(fabsf(x[u][i]) < INFINITY) ? 1.f : f, o[i]);
+          }
+        }
+      };
+      if (ns <= 2 * PH) {
+        add(std::integral_constant<int, 2>{}, phase);
+      } else {
+        for (int s0 = phase; s0 < ns; s0 += 8 * PH) add(std::integral_constant<int, 8>{}, s0);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float f = __builtin_amdgcn_exp2f(m[u].x - base);
-        if (s0 + u * PH < ns) {
-          sum = __builtin_fmaf(m[u].y, f, sum);
+      for (int k = LR; k < 64; k <<= 1) {
+        sum += __shfl_xor(sum, k);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[u][i], f, o[i]);
-        }
+        for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], k);
       }
     };
-    if (ns <= 2 * PH) {
-      add(std::integral_constant<int, 2>{}, phase);
-    } else {
-      for (int s0 = phase; s0 < ns; s0 += 8 * PH) add(std::integral_constant<int, 8>{}, s0);
-    }
-#pragma unroll
-    for (int k = LR; k < 64; k <<= 1) {
-      sum += __shfl_xor(sum, k);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], k);
-    }
+    join(std::false_type{});
+    if (__any(!(fabsf(o[0]) + fabsf(o[1]) + fabsf(o[2]) + fabsf(o[3]) < INFINITY))) join(std::true_type{});
     const float inv = 1.f / sum;
     const int row = t.r_first + r, token = over_group(p, row);
     uint16_t* to = p.out + ((size_t)(t.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;

@@ -54,19 +54,6 @@ struct AttnRowsLds {
   ShareScan<NW * 64> scan;
 };
 
-// Eight bf16 with zero in place of infinities and NaN, for their product with the
-// remainders of probabilities: a remainder is zero or of either sign, so an infinite
-// value times one would be NaN where the value times the probability is infinite.
-__device__ __forceinline__ u32x4_t finite(u32x4_t v) {
-  u32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = v[i];
-    r[i] = ((x & 0x7F80u) == 0x7F80u ? 0u : x & 0xFFFFu) | ((x & 0x7F800000u) == 0x7F800000u ? 0u : x & 0xFFFF0000u);
-  }
-  return r;
-}
-
 }  // namespace
 
 // Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1
@@ -298,8 +285,10 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       }
       const bool masked = uniform((p.window && k0 < it.cached + t.t_last - p.window + 1) || k0 < t.begin ||
                                   k0 + 32 > min(s_end, p.causal ? it.cached + t.t_first + 1 : t.end));
+      uint32_t sees[MT];   // SAFE: bit e of positions whose weight is more than zero, be it too small for fp32
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
+        sees[mt] = 0;
         if (masked) {
           // positions lo .. min(hi, s_end - 1), counted from lo
           const uint32_t seen = max(min(hi[mt], s_end - 1) - lo[mt] + 1, 0), first = k0 + 4 * j - lo[mt];
@@ -318,7 +307,9 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
           m[mt] = more ? mx : m[mt];
           l[mt] *= alpha;
 #pragma unroll
-          for (int n = 0; n < ND; ++n) acc[mt][n] *= alpha;
+          for (int n = 0; n < ND; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mt][n][i] = SAFE ? times(acc[mt][n][i], alpha) : acc[mt][n][i] * alpha;
         }
         // a row that has seen nothing yet keeps -infinity; its weights are 0
         const float base = m[mt] == -INFINITY ? 0.f : m[mt];
@@ -326,13 +317,25 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][e >> 2][e & 3], cs, -base));
-          if (SAFE) x = rep[mt].weight(x);
+          if (SAFE) {
+            sees[mt] |= (uint32_t)(sc[mt][e >> 2][e & 3] > -INFINITY) << e;
+            x = rep[mt].weight(x);
+          }
           sc[mt][e >> 2][e & 3] = x;
           sum += x;
         }
         l[mt] += sum;
       }
       u32x4_t pf[MT][2];    // probabilities: value and remainder
+      // SAFE: the product of a strip's values with row tile mt's weights, infinities and NaN apart
+      auto product = [&](u32x4_t vf, int mt, float4_t sum) {
+        uint32_t one[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) one[e] = sees[mt] >> e & 1 ? 0x3F80u : 0u;
+        const u32x4_t of = {one[0] | one[1] << 16, one[2] | one[3] << 16, one[4] | one[5] << 16, one[6] | one[7] << 16};
+        const u32x4_t v = finite(vf);
+        return mfma16x16x32_bf16(vf ^ v, of, mfma16x16x32_bf16(v, pf[mt][1], mfma16x16x32_bf16(v, pf[mt][0], sum)));
+      };
       auto split_p = [&](int mt, int run) {
 #pragma clang fp contract(off)   // the same remainder whatever the code around it: not one of an unrounded product
         uint32_t a[4], b[4];
@@ -349,9 +352,14 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
             const int e = 2 * g + u;
             x[u] = sc[mt][e >> 2][e & 3];
             if constexpr (FP8) {
-              x[u] *= vs[e >> 2][e & 3];
-              const int pos = k0 + 16 * (e >> 2) + 4 * j + (e & 3);
-              if (SAFE && (pos > hi[mt] || pos < lo[mt] || pos >= s_end)) x[u] = 0.f;   // the scale may be NaN
+              const float v = vs[e >> 2][e & 3];
+              if (!SAFE) {
+                x[u] *= v;
+              } else {   // the scale of a position that the row does not see may be an infinity or NaN
+                const int pos = k0 + 16 * (e >> 2) + 4 * j + (e & 3);
+                const bool far = !(fabsf(v) < INFINITY) && (sees[mt] >> e & 1);
+                x[u] = pos > hi[mt] || pos < lo[mt] || pos >= s_end ? 0.f : far ? v : x[u] * v;
+              }
             }
           }
           a[g] = f2bf2_rn(x[0], x[1]);
@@ -394,8 +402,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
             acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][0], acc[mt][n]);
             acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][1], acc[mt][n]);
           } else if (!masked) {
-            acc[mt][n] = mfma16x16x32_bf16(vf, pf[mt][0], acc[mt][n]);
-            acc[mt][n] = mfma16x16x32_bf16(finite(vf), pf[mt][1], acc[mt][n]);
+            acc[mt][n] = product(vf, mt, acc[mt][n]);
           } else {
             // token by token, with the values it does not see set to zero
 #pragma unroll 1
@@ -411,7 +418,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
               const uint32_t v0 = vf.x, v1 = vf.y, v2 = vf.z, v3 = vf.w;
               const u32x4_t vs = {v0 & (keep[0] | keep[1] << 16), v1 & (keep[2] | keep[3] << 16),
                                   v2 & (keep[4] | keep[5] << 16), v3 & (keep[6] | keep[7] << 16)};
-              const float4_t with = mfma16x16x32_bf16(finite(vs), pf[mt][1], mfma16x16x32_bf16(vs, pf[mt][0], acc[mt][n]));
+              const float4_t with = product(vs, mt, acc[mt][n]);
               if (tt == tok[mt]) acc[mt][n] = with;
             }
           }
@@ -470,7 +477,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       const float f = __builtin_amdgcn_exp2f(lds.w_m[w][r] - base);
       const float4_t x = *reinterpret_cast<const float4_t*>(reinterpret_cast<const float*>(&ring[w][0][0][0]) + r * OS + d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+      for (int i = 0; i < 4; ++i) o[i] = SAFE && !(fabsf(x[i]) < INFINITY) ? o[i] + x[i] : __builtin_fmaf(x[i], f, o[i]);
       sum = __builtin_fmaf(lds.w_l[w][r], f, sum);
     }
     if (slot < 0) {

@@ -369,15 +369,17 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
           for (int n = 0; n < ND; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[n][e] *= alpha;
+            for (int e = 0; e < 16; ++e) acc[n][e] = SAFE ? times(acc[n][e], alpha) : acc[n][e] * alpha;
         }
         // a row that has seen nothing yet keeps -infinity; its weights are 0
         const float base = m == -INFINITY ? 0.f : m;
         float sum = 0.f;
+        uint32_t sees = 0;   // SAFE: bit 16 nb + e of positions whose weight is more than zero, be it too small for fp32
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
+            if (SAFE) sees |= (uint32_t)(sc[nb][e] > -INFINITY) << (16 * nb + e);
             sc[nb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nb][e], cs, -base));
             if (SAFE) sc[nb][e] = rep.weight(sc[nb][e]);
             sum += sc[nb][e];
@@ -394,15 +396,14 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
             const float4_t v0 = *reinterpret_cast<const float4_t*>(&ring_s[at][1][run][key0]);
             const float4_t v1 = *reinterpret_cast<const float4_t*>(&ring_s[at][1][run][key0 + 8]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              w[e] *= v0[e];
-              w[4 + e] *= v1[e];
-            }
-            if (SAFE) {   // the scale of a position that the row does not see may be NaN
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 8; ++e) {
+              const float v = e < 4 ? v0[e] : v1[e - 4];
+              if (!SAFE) {
+                w[e] *= v;
+              } else {   // the scale of a position that the row does not see may be an infinity or NaN
                 const int pos = k0 + key0 + e % 4 + 8 * (e / 4);
-                if (pos > hi || pos < lo || pos >= s_end) w[e] = 0.f;
+                const bool far = !(fabsf(v) < INFINITY) && (sees >> (16 * nb + 8 * ks + e) & 1);
+                w[e] = pos > hi || pos < lo || pos >= s_end ? 0.f : far ? v : w[e] * v;
               }
             }
           }
@@ -417,6 +418,15 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           const uint64_t w1 = lds_read_tr16(lv + ((key + 8) * CH + ((c0 >> 3) ^ swz_t<DP>(key + 8))) * 16 + (c0 & 7) * 2);
           return u32x4_t{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
         };
+        // SAFE: the product of strip n's values vf with the weights, infinities and NaN apart
+        auto product = [&](u32x4_t vf, u32x4_t pf, int nb, int ks, float16_t sum) {
+          uint32_t one[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) one[e] = sees >> (16 * nb + 8 * ks + e) & 1 ? 0x3F80u : 0u;
+          const u32x4_t of = {one[0] | one[1] << 16, one[2] | one[3] << 16, one[4] | one[5] << 16, one[6] | one[7] << 16};
+          const u32x4_t v = finite(vf);
+          return mfma32x32x16_bf16(vf ^ v, of, mfma32x32x16_bf16(v, pf, sum));
+        };
         if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         if (!SAFE || !masked) {
 #pragma unroll
@@ -428,7 +438,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
               for (int n = 0; n < ND; ++n) {
                 if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
                 const u32x4_t vf = values(nb, ks, n);
-                acc[n] = mfma32x32x16_bf16(vf, pf, acc[n]);
+                acc[n] = SAFE ? product(vf, pf, nb, ks, acc[n]) : mfma32x32x16_bf16(vf, pf, acc[n]);
               }
             }
         } else {
@@ -453,7 +463,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
                   }
                   const u32x4_t vs = {vf.x & (keep[0] | keep[1] << 16), vf.y & (keep[2] | keep[3] << 16),
                                       vf.z & (keep[4] | keep[5] << 16), vf.w & (keep[6] | keep[7] << 16)};
-                  const float16_t with = mfma32x32x16_bf16(vs, pf, acc[n]);
+                  const float16_t with = product(vs, pf, nb, ks, acc[n]);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) acc[n][e] = tt == tok ? with[e] : acc[n][e];
                 }

@@ -165,3 +165,33 @@ def test_large_values_beside_an_infinite_one(lib, gpu, form, gran, bad):
     got, hidden = run(lib, d, 0.125), blind(d, at, 0)
     compare(d, got, exact(d, 0.125), form)
     assert np.isfinite(bf16v(got)[hidden]).all() and np.array_equal(got[hidden], clean[hidden])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("gran", [0, 64])
+@pytest.mark.parametrize("order", ["first", "last"])
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+def test_an_infinite_value_counts_however_small_its_weight(lib, gpu, form, gran, order, bad):
+    """A position whose weight is e^-200 of the others', less than fp32 holds: before all scores that
+    are so much larger (the row's sums are rescaled, in a block, between waves or between parts),
+    or behind them."""
+    d = case(55, form, 128, gran)
+    S = d.blocks.shape[3]
+    n = int(d.cache_lengths[0]) + int(d.row_offsets[1])
+    at = np.arange(n)
+    small = int(d.cache_lengths[0]) // 2 if order == "first" else 0   # positions with a score of 0
+    k = np.zeros((n, d.blocks.shape[4], 128))
+    k[small:, :, 0] = 200.0
+    spot = small // 3 if order == "first" else int(d.cache_lengths[0]) - 2
+    k[spot] = 0.0
+    page = d.page_table[0, at // S]
+    if gran:
+        d.blocks[1, 0, page, at % S] = synth.e4m3_codes(k)
+        d.scales[1, 0, page, at % S] = 1.0
+    else:
+        d.blocks[1, 0, page, at % S] = synth.bf16_bits(k)
+    d.q[:int(d.row_offsets[1])] = synth.bf16_bits(np.broadcast_to(np.eye(128)[0], d.q[:int(d.row_offsets[1])].shape))
+    put(d, 1, spot, float(bad))
+    ref = exact(d, 1.0)
+    assert not np.isfinite(ref[0][0]).all()
+    compare(d, run(lib, d, 1.0), ref, form)
