@@ -41,14 +41,34 @@ constexpr float kSlack = 8.f;    // log2 of how far a weight may exceed its row'
 // again (by the pass that selects values), its weights divided by a power of two that makes
 // their sum over all positions at most 1/4, so that the sums, those of the other parts
 // included, stay in range; the reference that goes with them says so.
+//
+// A weight's exponent is score * c - m in one rounding (c: scale and base), m the rounded
+// product of the row's largest score: for that score it is m's rounding error, which no
+// longer is about zero once scores pass 2^24, and takes all weights out of range from
+// about 2^30 on. A row whose weights' sum has gone far from one is computed again with
+// the product rounded in both places alike.
 constexpr float kSumsMost = 0x1p116f;
-constexpr int kRepeats = 2;   // runs of the pass that selects values: a row changes once
+constexpr int kRepeats = 3;   // runs of the pass that selects values: each row may change twice
+// m: reference, sum: of the weights that go with it, of all positions (at least one where it
+// is finite, but for that error)
+__device__ __forceinline__ bool weights_off(float m, float sum) { return m > -INFINITY && !(sum > 0x1p-60f && sum < 0x1p60f); }
 struct AttnRepeat {
+  bool apart = false;         // exponents with the product rounded by itself
   int shift = 0;              // log2 of what the row's weights are divided by
+  __device__ __forceinline__ float exponent(float score, float c, float m) const {
+#pragma clang fp contract(off)
+    const float x = score * c;
+    return apart ? x - m : __builtin_fmaf(score, c, -m);
+  }
   __device__ __forceinline__ float weight(float w) const { return __builtin_amdgcn_ldexpf(w, -shift); }
   __device__ __forceinline__ float reference(float m) const { return m + (float)shift; }
-  // large: some accumulator is not below kSumsMost. Whether the row has to be computed again.
-  __device__ __forceinline__ bool again(bool large, int positions) {
+  // off: weights_off; large: some accumulator is not below kSumsMost. Whether the row has to
+  // be computed again.
+  __device__ __forceinline__ bool again(bool off, bool large, int positions) {
+    if (off && !apart) {
+      apart = true;
+      return true;
+    }
     if (!large || shift) return false;
     shift = 42 - __builtin_clz(positions);   // weights are 2^8 at most
     return true;

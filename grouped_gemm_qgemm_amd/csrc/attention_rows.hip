@@ -59,8 +59,8 @@ struct AttnRowsLds {
 // Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1
 // and go to that slot of the workspace else. GRAN: head-dim elements per scale of an
 // e4m3 cache, 0 for bf16. SAFE: values are selected per token. Returns whether some
-// row has to be computed again (without SAFE: some accumulator is too large, an infinity
-// or NaN; with it: as `rep`, the state of this lane's rows in this wave, says), for the
+// row has to be computed again (without SAFE: sums are too large, infinities, NaN or
+// zero; with it: as `rep`, the state of this lane's rows in this wave, says), for the
 // whole workgroup, and then has written nothing.
 template <int DP, int GRAN, int MT, int NW, int NST, bool SAFE>
 __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h0, int hw, int c_first, int c_end, int slot,
@@ -316,7 +316,8 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
         float sum = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[mt][e >> 2][e & 3], cs, -base));
+          float x = sc[mt][e >> 2][e & 3];
+          x = __builtin_amdgcn_exp2f(SAFE ? rep[mt].exponent(x, cs, base) : __builtin_fmaf(x, cs, -base));
           if (SAFE) {
             sees[mt] |= (uint32_t)(sc[mt][e >> 2][e & 3] > -INFINITY) << e;
             x = rep[mt].weight(x);
@@ -434,11 +435,16 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) far |= !(fabsf(acc[mt][n][i]) < kSumsMost);
+    l[mt] += __shfl_xor(l[mt], 16);
+    l[mt] += __shfl_xor(l[mt], 32);
     if (SAFE) {
       far |= __shfl_xor(far, 16);
       far |= __shfl_xor(far, 32);
-      m[mt] = rep[mt].reference(m[mt]);
-      far = rep[mt].again(far, t.end - t.start);
+      const float with = rep[mt].reference(m[mt]);
+      far = rep[mt].again(weights_off(m[mt], l[mt]), far, t.end - t.start);
+      m[mt] = with;
+    } else {
+      far |= weights_off(m[mt], l[mt]);
     }
     off |= far;
   }
@@ -449,8 +455,6 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
   float* mine = reinterpret_cast<float*>(&ring[wave][0][0][0]);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    l[mt] += __shfl_xor(l[mt], 16);
-    l[mt] += __shfl_xor(l[mt], 32);
     if (j == 0) {
       lds.w_m[wave][16 * mt + col] = m[mt];
       lds.w_l[wave][16 * mt + col] = l[mt];

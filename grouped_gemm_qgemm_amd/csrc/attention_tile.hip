@@ -41,7 +41,7 @@
 // Its value row is still multiplied, by zero: where it holds an infinity or NaN
 // the row's output would turn NaN. So a tile whose accumulators are not finite, or so
 // large that sums of them may not be, is computed again with the values selected per
-// token (and, where large ones are left, smaller weights: AttnRepeat).
+// token (and, where that does not help, other weights: AttnRepeat).
 #include "attention_common.h"
 
 namespace qg {
@@ -75,7 +75,7 @@ struct AttnTileLds {
 
 // One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
 // values are selected per token. Returns whether some row has to be computed again
-// (without SAFE: some accumulator is too large, an infinity or NaN; with it: as `rep`, the
+// (without SAFE: sums are too large, infinities, NaN or zero; with it: as `rep`, the
 // state of this lane's row, says), for the whole workgroup, and then has written nothing.
 template <int DP, int GRAN, bool SAFE>
 __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds, AttnRepeat& rep) {
@@ -151,6 +151,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 
   float16_t acc[ND];
   float m = -INFINITY, l = 0.f;   // reference of the weights' exponents (base 2), this lane's share of their sum
+  float sum;                      // the row's
   {
 #pragma unroll
     for (int n = 0; n < ND; ++n)
@@ -373,18 +374,18 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
         }
         // a row that has seen nothing yet keeps -infinity; its weights are 0
         const float base = m == -INFINITY ? 0.f : m;
-        float sum = 0.f;
+        float l_block = 0.f;
         uint32_t sees = 0;   // SAFE: bit 16 nb + e of positions whose weight is more than zero, be it too small for fp32
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             if (SAFE) sees |= (uint32_t)(sc[nb][e] > -INFINITY) << (16 * nb + e);
-            sc[nb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[nb][e], cs, -base));
+            sc[nb][e] = __builtin_amdgcn_exp2f(SAFE ? rep.exponent(sc[nb][e], cs, base) : __builtin_fmaf(sc[nb][e], cs, -base));
             if (SAFE) sc[nb][e] = rep.weight(sc[nb][e]);
-            sum += sc[nb][e];
+            l_block += sc[nb][e];
           }
-        l += sum;
+        l += l_block;
 
         // weights of 16 positions as the B operand; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
         auto weights = [&](int nb, int ks, int run) {
@@ -480,7 +481,9 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     for (int n = 0; n < ND; ++n)
 #pragma unroll
       for (int e = 0; e < 16; ++e) off |= !(fabsf(acc[n][e]) < kSumsMost);
-    if (SAFE) off = rep.again(off | __shfl_xor(off, 32), t.end - t.start);
+    sum = l + __shfl_xor(l, 32);
+    if (SAFE) off = rep.again(weights_off(m, sum), off | __shfl_xor(off, 32), t.end - t.start);
+    else off |= weights_off(m, sum);
     off = __any(off);
     if (lane == 0) lds.w_off[wave] = off;
     __syncthreads();
@@ -492,7 +495,6 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 
   const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
   float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(p.bm, DP);
-  const float sum = l + __shfl_xor(l, 32);
   const int r = wave * 32 + col;
   if (r >= t.r_count) return false;
   if (alone) {

@@ -1,5 +1,5 @@
 """attention_ragged_paged where numbers are extreme: what a row does not see must not change a
-bit of it, and large finite values must give the formula's finite results."""
+bit of it, and large finite values and scores must give the formula's finite results."""
 import numpy as np
 import pytest
 import torch
@@ -195,3 +195,37 @@ def test_an_infinite_value_counts_however_small_its_weight(lib, gpu, form, gran,
     ref = exact(d, 1.0)
     assert not np.isfinite(ref[0][0]).all()
     compare(d, run(lib, d, 1.0), ref, form)
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("gran", [0, 64])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_scores_far_beyond_one(lib, gpu, form, gran, sign, dim):
+    """Scores of 2^40 and more, exact in fp32 (one product of two short numbers each), so far apart
+    that all weight is on the largest, or even on those that share it: their mean comes out.
+
+    The weights are 1 or 0, so what is rounded is the sum over equal ones (N + 1 roundings of 2^-24
+    of the mean of |v|, as the division) and the result to bf16 (2^-8); with an e4m3 cache also
+    the weight times its value's scale, to bf16 in the kernel for many rows: at most 2^-8 of each
+    |v|, so 2^-8 of their mean, which the result's rounding then sees (a factor 1 + 2^-8)."""
+    d = case(53, form, dim, gran)
+    rng = np.random.default_rng(8)
+    d.q[:] = synth.bf16_bits(np.broadcast_to(sign * np.eye(dim)[0] * 2.0**20, d.q.shape))
+    keys = d.blocks[1, 0]
+    k = np.zeros(keys.shape)
+    k[..., 0] = 1 + rng.integers(0, 8, keys.shape[:-1]) / 8
+    if gran:
+        held = keys != 0x7F
+        d.blocks[1, 0] = np.where(held, synth.e4m3_codes(k), 0x7F)
+        d.scales[1, 0] = np.where(np.isnan(d.scales[1, 0]), np.nan, 2.0**20).astype(np.float32)
+    else:
+        d.blocks[1, 0] = np.where(keys != 0xFFFF, synth.bf16_bits(k * 2.0**20), 0xFFFF)
+    out, spread, _ = exact(d, 1.0)
+    n = int((d.cache_lengths.astype(np.int64) + np.diff(d.row_offsets.astype(np.int64))).max())
+    got = bf16v(run(lib, d, 1.0))
+    err = np.abs(got - out)
+    tol = 2.0**-8 * np.abs(out) + (n + 4) * 2.0**-23 * spread
+    if gran:
+        tol += 2.0**-8 * (1 + 2.0**-8) * spread
+    good = bool((err <= tol).all())
+    assert good, (int(np.isnan(got).sum()), float(np.nanmax(err)))
