@@ -457,7 +457,8 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   if (D % 8 != 0) return QG_ERR_ALIGN;
   if (fp8 && (st = check_cache_scales(kv)) != QG_OK) return st;
   if ((int64_t)layer_idx >= L) return QG_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale) || window < 0) return QG_ERR_INVALID_ARG;
+  // (log2 e: the kernels' exponents have base 2)
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f) || window < 0) return QG_ERR_INVALID_ARG;
   if (window > 0 && !causal) return QG_ERR_UNSUPPORTED;
   if (D > 256) return QG_ERR_UNSUPPORTED;
   if (T == 0 || B == 0 || Hq == 0 || D == 0) return QG_OK;

@@ -413,7 +413,7 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
  *                                    offs[B] on are left as they were
  *   kv                the paged cache (bf16, or e4m3 codes with their scales), read only
  *   layer_idx         < L (QG_ERR_INVALID_ARG otherwise)
- *   scale             finite and > 0 (QG_ERR_INVALID_ARG otherwise)
+ *   scale             > 0 and below 2^128 / log2 e, about 2.358e38 (QG_ERR_INVALID_ARG otherwise)
  *   causal            nonzero: positions 0 .. p; 0: 0 .. cache_lengths[b] + n_b - 1, the whole
  *                     sequence with all its new tokens
  *   window            0, or the number of positions a token sees, itself included
