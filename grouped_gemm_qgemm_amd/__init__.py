@@ -184,6 +184,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _int32(name: str, v: int, most: int = 0x7FFFFFFF) -> int:
+    """v, which ctypes would cut to 32 bits without a word."""
+    if not -0x80000000 <= v <= most:
+        raise ValueError(f"{name} does not fit 32 bits")
+    return v
+
+
 def _check(st: int):
     if st != QG.OK:
         raise QgError(st, status_string(st))
@@ -316,7 +323,7 @@ def _kv_call(fn, hidden, input_row_offsets, weight, input_scale, weight_scale, k
     kv = _paged_kv(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity)
     st = fn(ctypes.byref(describe(hidden)), ctypes.byref(describe(input_row_offsets, _u32(input_row_offsets))),
             ctypes.byref(describe(weight)), ctypes.byref(describe(input_scale)),
-            ctypes.byref(describe(weight_scale)), gran, ctypes.byref(kv), int(layer_idx), _stream(stream))
+            ctypes.byref(describe(weight_scale)), gran, ctypes.byref(kv), _int32("layer_idx", int(layer_idx), 0xFFFFFFFF), _stream(stream))
     if raise_on_error:
         _check(st)
     return st
@@ -411,7 +418,7 @@ def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_l
     u32 = _TABLE_DTYPE
     st = _launch(lib.tables_ragged_paged, dev, stream, _record(input_row_offsets, u32), _record(slot_map),
                  _record(page_table, u32), _record(result, u32), _record(cache_lengths, u32), _record(new_lengths, u32),
-                 _record(free_pages, u32), _record(free_count, u32), page_size)
+                 _record(free_pages, u32), _record(free_count, u32), _int32("page_size", page_size))
     if raise_on_error:
         _check(st)
     return st
@@ -452,7 +459,7 @@ def attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, 
                            0 if page_table is None else page_table.data_ptr(), pages)
               + (_NO_TENSOR if kv_scales is None else _record(kv_scales)) + _KV_GRANULARITY(quantization_granularity))
     st = _launch(lib.attention_ragged_paged, dev, stream, _record(out), _record(q), _record(input_row_offsets, _TABLE_DTYPE),
-                 kv, layer_idx, scale, 1 if causal else 0, window, _record(workspace))
+                 kv, _int32("layer_idx", layer_idx, 0xFFFFFFFF), scale, 1 if causal else 0, _int32("window", window), _record(workspace))
     if raise_on_error:
         _check(st)
     return st

@@ -17,3 +17,47 @@ def test_a_scale_whose_base_2_form_is_infinite_is_refused(lib):
     assert attn_call(lib, bb, scale=2.0**128 / 1.4426950408889634 * (1 + 1e-6)) == QG.ERR_INVALID_ARG
     assert attn_call(lib, bb, scale=2.0**127, out=(0, 4, 64), q_=(0, 4, 64)) == QG.OK
     assert attn_call(lib, bb, scale=math.ldexp(1.0, -149), out=(0, 4, 64), q_=(0, 4, 64)) == QG.OK
+
+
+WIDE = (2**31, 2**32, 2**32 + 5, -2**31 - 1, -2**32)
+
+
+def test_whole_numbers_that_do_not_fit_are_refused_not_cut(monkeypatch):
+    """A window of 2^32 is not one of 0, a page of 2^32 + 16 slots not one of 16, layer 2^32 not
+    layer 0: the binding refuses them before the library is called."""
+    def reached(*a, **k):
+        raise AssertionError("the library was called")
+
+    class Library:
+        def __getattr__(self, name):
+            return reached
+    monkeypatch.setattr(q, "load", lambda: Library())
+    monkeypatch.setattr(q, "_device_of", lambda tensors: None)
+    monkeypatch.setattr(q, "_launch", reached)
+    monkeypatch.setattr(q, "_stream", lambda stream: None)
+    t = torch.zeros(4, dtype=torch.int32)
+    x = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    blocks = torch.zeros(1, 2, 1, 16, 1, 64, dtype=torch.bfloat16)
+
+    def attention(layer=0, window=0):
+        q.attention_ragged_paged(x, x, t[:2], blocks, t[:1], t[:1].view(1, 1), layer, 1.0, torch.zeros(4), window=window)
+
+    def tables(page):
+        q.tables_ragged_paged(torch.zeros(5, dtype=torch.int32), None, torch.zeros(4, 2, dtype=torch.int32),
+                              torch.zeros(2, dtype=torch.int32), t, t, t, t[:1], page)
+
+    def project(fn, layer):
+        fn(x[0], t[:2], x[0], x[0], x[0], blocks, t[:1], t[:1].view(1, 1), layer)
+
+    for v in WIDE:
+        for call in (lambda: attention(window=v), lambda: tables(v)):
+            with pytest.raises(ValueError):
+                call()
+    for v in (2**32, 2**32 + 1, -2**32):
+        for call in (lambda: attention(layer=v), lambda: project(q.k_matmul_ragged_paged_scale, v),
+                     lambda: project(q.kv_matmul_ragged_paged_scale, v)):
+            with pytest.raises(ValueError):
+                call()
+    for call in (attention, lambda: tables(16), lambda: project(q.k_matmul_ragged_paged_scale, 0), lambda: attention(layer=-1)):
+        with pytest.raises(AssertionError):
+            call()
