@@ -20,6 +20,8 @@ namespace qg {
 namespace {
 
 constexpr int JT = 256;
+// of 256 threads: a launch has less than 2^32 of those
+constexpr long long kMostWorkgroups = (1ll << 24) - 1;
 constexpr int kRowsMost = 512, kRowsStep = 32, kRowsHeads = 4;
 // Items of the kernel for many rows, two per CU (one per CU: 1000 tokens after 32000 688 us
 // against 538; four: eight prompts of 1 to 1024 tokens 75 us against 63), of at least 256
@@ -181,7 +183,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const long long wide = std::min<long long>(p.target / groups, tiles * units);
     const long long narrow = std::min<long long>(std::max(p.target / p.hkv, 1), tiles * units);
     const long long grid = std::max((wide + 7) / 8 * 8 * groups, (narrow + 7) / 8 * 8 * p.hkv);
-    if (grid > INT32_MAX) return hipErrorNotSupported;
+    if (grid > kMostWorkgroups) return hipErrorNotSupported;
     const hipError_t e = launch_attention_rows(p, mt, (unsigned)grid, stream);
     const long long pieces = std::max(wide, narrow);
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
@@ -194,7 +196,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   // item return.
   const long long chunks = (room + p.min_chunk - 1) / p.min_chunk;
   const long long items = std::min(tiles + p.target / p.hkv + 1, chunks < tiles + p.target ? tiles * chunks : (long long)INT64_MAX);
-  if (items * p.hkv > INT32_MAX) return hipErrorNotSupported;
+  if (items > kMostWorkgroups / p.hkv) return hipErrorNotSupported;
   const hipError_t e = launch_attention_tiles(p, (unsigned)(items * p.hkv), stream);
   // tiles that are cut have at least two slots each, of fewer than 2 target
   return e != hipSuccess || chunks <= 1 ? e : launch_join(p, std::min(tiles, (long long)(p.target / p.hkv + 1)), stream);

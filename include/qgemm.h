@@ -429,7 +429,8 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
  * probabilities are rounded to bf16 for their product with the values, and the
  * result to bf16 (nearest-even). The result does not depend on timing: the same
  * call gives the same bits. Offsets, lengths and page ids are not re-validated on
- * the device.
+ * the device. Sizes that 32 bits do not count, or that need 2^24 workgroups or more
+ * (T * Hq / 128 + B * Hkv in the order of 2^24), are QG_ERR_UNSUPPORTED.
  */
 int64_t attention_ragged_paged_workspace(int64_t T, int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
                                          int64_t head_dim);

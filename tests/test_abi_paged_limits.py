@@ -8,7 +8,7 @@ import torch
 import grouped_gemm_qgemm_amd as q
 from grouped_gemm_qgemm_amd import QG
 from test_abi import Buf
-from test_abi_paged import attn_call, lib
+from test_abi_paged import attn_call, kv_of, lib, ref
 
 
 def test_a_scale_whose_base_2_form_is_infinite_is_refused(lib):
@@ -61,3 +61,22 @@ def test_whole_numbers_that_do_not_fit_are_refused_not_cut(monkeypatch):
     for call in (attention, lambda: tables(16), lambda: project(q.k_matmul_ragged_paged_scale, 0), lambda: attention(layer=-1)):
         with pytest.raises(AssertionError):
             call()
+
+
+def test_more_workgroups_than_a_launch_takes_are_refused(lib):
+    """A launch has less than 2^32 threads. 2^20 sequences on 16 heads with 33 rows each on average
+    may need more than 2^24 workgroups of 256; one token on 2^22 heads 2^25."""
+    bb = Buf()
+
+    def call(T, B, heads, dim, max_pages):
+        t = [bb.t((1, 1, dim), QG.BF16), bb.t((1, 1, dim), QG.BF16), bb.t((1,), QG.U32), bb.t((1,), QG.F32)]
+        for x in t[:2]:   # (only looked at, not allocated)
+            x.shape[0], x.shape[1] = T, heads
+        t[2].shape[0] = B + 1
+        t[3].shape[0] = 1 << 45
+        kv = kv_of(bb, Hkv=1, D=dim, gran=0, maxp=max_pages)
+        kv.blocks.shape[4] = heads
+        return lib.attention_ragged_paged(ref(t[0]), ref(t[1]), ref(t[2]), ref(kv), 0, 0.125, 1, 0, ref(t[3]), None)
+
+    assert call(33 << 20, 1 << 20, 16, 64, 64) == QG.ERR_UNSUPPORTED
+    assert call(1, 1, 1 << 22, 8, 64) == QG.ERR_UNSUPPORTED
