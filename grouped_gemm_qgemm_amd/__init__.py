@@ -412,7 +412,8 @@ def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_l
     """Row offsets [B + 1], new page table entries (page_table [B, W], updated) and slot map
     [T] (or None) of one step, from cache_lengths and new_lengths [B] and a stack of free
     pages (free_pages [F], free_count [1]). result [2]: pages left, status (0: built; else
-    1 too few pages | 2 a sequence past W pages | 4 more tokens than slots, nothing written)."""
+    1 too few pages | 2 a sequence past W pages | 4 more tokens than slots, nothing written:
+    the calls that take the tables must not run on them then)."""
     lib = load()
     dev = _device_of((input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages, free_count))
     u32 = _TABLE_DTYPE

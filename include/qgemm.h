@@ -362,7 +362,7 @@ qg_status kv_matmul_ragged_paged_scale(const qg_tensor* hidden, const qg_tensor*
  * device from the sequences' lengths
  *
  * Writes what k_matmul_ragged_paged_scale, kv_matmul_ragged_paged_scale and
- * attention_ragged_paged take as given, so that a step needs no host round trip
+ * attention_ragged_paged take as given; building them needs no host round trip
  * (and can be captured and replayed). With c_b = cache_lengths[b] tokens cached,
  * n_b = new_lengths[b] to be added and S = page_size:
  *
@@ -384,8 +384,12 @@ qg_status kv_matmul_ragged_paged_scale(const qg_tensor* hidden, const qg_tensor*
  *   1  the stack holds too few pages (or free_count[0] > F)
  *   2  a sequence with new tokens is longer than W * S
  *   4  there are more tokens than slot_map has elements (2^31 - 1 without one)
- * and then nothing but `result` is written, with result[0] = free_count[0]: the
- * caller looks at it before the tables are used. Page ids are not checked; they
+ * and then nothing but `result` is written, with result[0] = free_count[0]. The
+ * tables are then an earlier step's, or were never filled, and the calls that take
+ * them check no page id: they must not run on them. So a caller either reads `result`
+ * before it enqueues those calls, or enqueues (or captures) the whole step knowing
+ * that it fits; the lengths and the number of free pages, which each call changes by
+ * what is written above, tell that without asking the device. Page ids are not checked; they
  * are below 2^31 / S. cache_lengths is not updated. B above 8192, or (W + 1) * S
  * above 2^31 - 1, is QG_ERR_UNSUPPORTED; B = 0 is a no-op.
  */

@@ -140,3 +140,32 @@ def test_other_stream_and_replays(lib, gpu):
         assert np.array_equal(dev["slots"].cpu().numpy()[:len(slots)], slots)
         assert host(pair[0]).tolist() == [count, 0]
         _ = (torch.ones(1000, device="cuda") * 2).sum().item()   # the program's own work in between
+
+
+def test_a_captured_step_that_no_longer_fits_leaves_the_tables(lib, gpu):
+    """Replayed until the stack is empty: from there on every replay says so and writes nothing else."""
+    c = case(7, [5, 3], [0, 9], 4, slack=4, spare=40)
+    dev = run(lib, c)
+    pair = [dev32(np.array([c["count"], 0], np.int32)), dev32(np.zeros(2, np.int32))]
+    dev["table"].copy_(dev32(c["table"]))
+    dev["cached"].copy_(dev32(c["cached"]))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.tables_ragged_paged(dev["offsets"], dev["slots"], dev["table"], pair[1], dev["cached"], dev["fresh"], dev["free"],
+                                pair[0][:1], c["page"])
+        pair[0].copy_(pair[1])
+        dev["cached"].add_(dev["fresh"])
+    table, cached, count, kept = c["table"], c["cached"].astype(np.int64), c["count"], None
+    for turn in range(8):
+        g.replay()
+        torch.cuda.synchronize()
+        offs, built, slots, (count, status) = oracle.tables_ragged_paged(table, cached, c["new"], c["free"], count, c["page"],
+                                                                         c["slots"])
+        cached = cached + c["new"]
+        assert host(pair[0]).tolist() == [count, status]
+        if status == 0:
+            table, kept = built, (offs, slots)
+        assert np.array_equal(host(dev["table"]), table)
+        assert np.array_equal(host(dev["offsets"]), kept[0]) and np.array_equal(dev["slots"].cpu().numpy()[:len(kept[1])], kept[1])
+    assert status == 1 and turn == 7
