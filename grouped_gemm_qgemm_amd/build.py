@@ -52,6 +52,10 @@ def _compile(src: str) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    # warnings, but for the host pass not knowing the target feature above
+    said = [line for line in r.stderr.splitlines() if "packed-fp32-ops" not in line and not line.endswith("warning generated when compiling for host.")]
+    if said:
+        print("\n".join(said), file=sys.stderr)
     return obj
 
 

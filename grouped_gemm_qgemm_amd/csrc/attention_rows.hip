@@ -516,8 +516,18 @@ __device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnI
       return;
 }
 
+// Workgroups per CU by LDS (160 KB), and the waves per SIMD that the registers are divided
+// for: two where LDS has room for eight waves per CU (all heads of 64, e4m3 of 128), else one.
+template <typename Lds>
+constexpr int attn_resident(int nw) {
+  const int by_lds = 163840 / (int)sizeof(Lds), by_registers = 8 / nw;
+  return by_lds < by_registers ? by_lds : by_registers;
+}
+template <typename Lds>
+constexpr int attn_waves(int nw) { return attn_resident<Lds>(nw) * nw >= 8 ? 2 : 1; }
+
 template <int DP, int GRAN, int MT, int NW, int NST>
-__global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) {
+__global__ __launch_bounds__(NW * 64, (attn_waves<AttnRowsLds<DP, GRAN, MT, NW, NST>>(NW))) void attention_rows_kernel(AttnArgs p) {
   __shared__ AttnRowsLds<DP, GRAN, MT, NW, NST> lds;
   AttnShare s = attn_share<NW * 64>(p, lds.scan);
   if (s.b < 0) return;
@@ -569,13 +579,13 @@ __global__ __launch_bounds__(NW * 64, 2) void attention_rows_kernel(AttnArgs p) 
 
 namespace {
 
-// f(kernel, waves per workgroup, LDS bytes) of the instance that serves a call.
+// f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call.
 template <typename F>
 void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
 #define QG_ATTN(DP, GRAN, NW, NST)                                                                              \
   do {                                                                                                          \
-    if (mt == 1) f(attention_rows_kernel<DP, GRAN, 1, NW, NST>, NW, sizeof(AttnRowsLds<DP, GRAN, 1, NW, NST>)); \
-    else f(attention_rows_kernel<DP, GRAN, 2, NW, NST>, NW, sizeof(AttnRowsLds<DP, GRAN, 2, NW, NST>));         \
+    if (mt == 1) f(attention_rows_kernel<DP, GRAN, 1, NW, NST>, NW, attn_resident<AttnRowsLds<DP, GRAN, 1, NW, NST>>(NW)); \
+    else f(attention_rows_kernel<DP, GRAN, 2, NW, NST>, NW, attn_resident<AttnRowsLds<DP, GRAN, 2, NW, NST>>(NW));         \
   } while (0)
   const int gran = p.fp8 ? p.gran : 0;
   if (p.d <= 64) {
@@ -599,17 +609,15 @@ void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
 }  // namespace
 
 void attention_rows_shape(AttnArgs& p, int mt) {
-  with_rows_kernel(p, mt, [&](auto, int nw, size_t lds) {
-    // resident workgroups: by LDS (160 KB per CU), and by registers (the kernels are built
-    // for two waves per SIMD)
-    p.target = p.num_cus * std::max(1, std::min((int)(163840 / lds), 8 / nw));
+  with_rows_kernel(p, mt, [&](auto, int nw, int resident) {
+    p.target = p.num_cus * resident;
     p.hw = nw;
     while (p.hkv % p.hw != 0) p.hw /= 2;
   });
 }
 
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream) {
-  with_rows_kernel(p, mt, [&](auto kernel, int nw, size_t) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
+  with_rows_kernel(p, mt, [&](auto kernel, int nw, int) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
   return hipGetLastError();
 }
 

@@ -425,7 +425,6 @@ __global__ __launch_bounds__(WM * 256) void kproj_bf16_kernel(
   for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   typedef int i32x2_t __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
   auto compute = [&](int kb, int buf) {
     float4_t part[MT][2];
 #pragma unroll
