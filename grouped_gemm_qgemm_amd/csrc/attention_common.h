@@ -386,8 +386,8 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
   s.cut.units = __builtin_amdgcn_readfirstlane(s.cut.units);
   // With much to read, a wave per head and neighbouring heads together (p.hw). With fewer
   // than kWideBlocks blocks per wave, all waves on one head: a quarter of the parts to
-  // join for the same time (single tokens, bf16: 8 sequences of 500 positions 16 us against
-  // 20, 16 of 2000 38 to 40 either way, 64 of 1 to 8192 222 us against 209).
+  // join (single tokens, bf16, one head against several: 8 sequences of 500 positions 12.7 us
+  // against 15.0, 16 of 2000 36 against 34, 32 of 2000 51 against 54, 64 of 1 to 8192 214 against 204).
   const bool wide = (unsigned long long)s.cut.units * (p.hkv / p.hw) >= (unsigned long long)kWideBlocks * p.target;
   s.hw = wide ? p.hw : 1;
   const int groups = wide ? p.hkv / p.hw : p.hkv, least = wide ? 1 : NT / 64;

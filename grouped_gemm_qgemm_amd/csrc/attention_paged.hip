@@ -23,9 +23,12 @@ constexpr int JT = 256;
 // of 256 threads: a launch has less than 2^32 of those
 constexpr long long kMostWorkgroups = (1ll << 24) - 1;
 constexpr int kRowsMost = 512, kRowsStep = 32, kRowsHeads = 4;
-// Items of the kernel for many rows, two per CU (one per CU: 1000 tokens after 32000 688 us
-// against 538; four: eight prompts of 1 to 1024 tokens 75 us against 63), of at least 256
-// positions (128 or 512: within 2 %).
+// Items of the kernel for many rows, two per CU (one per CU: 1000 tokens after 32000 685 us
+// against 517; four: eight prompts of 1 to 1024 tokens 54 us against 42, heads of 256 with a
+// window 302 against 272, though e4m3 chunks with runs of 32 381 against 407), of at least
+// 256 positions (128 or 512: level). A tile is cut only where it is longer than an even share
+// of all tiles' positions, so batches of several prompts are not: of those eight, played
+// through in launch order, the last workgroup ends after 16 blocks where the mean is 11.
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
@@ -159,15 +162,17 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   divide_by(p.page_size, p.div_mul, p.div_shift);
   divide_by(p.group, p.group_mul, p.group_shift);
   const long long rows = p.T * p.group;
-  // The kernel for few rows takes up to 16 rows per sequence and head on average (64
-  // sequences of one token: 207 us, 1.5 times that in tiles of 128 rows on bf16 and twice
-  // on e4m3), and up to 32 where there are many sequences (32 of 6 tokens on 4000
-  // positions, 4 heads to one: bf16 132 against 135 us, e4m3 90 against 125; on 500
-  // positions 28 against 37 and 33 against 39). With fewer, each is cut into many parts,
-  // whose records of 32 rows cost more than half-empty tiles (8 sequences: bf16 40 us
-  // against 52, e4m3 46 against 52), except for e4m3 heads of 256, which the kernel for
-  // many rows is slow at (126 us against 84). Beyond 32 rows it loses (32 sequences of 16
-  // tokens: bf16 191 us against 142, e4m3 141 against 133).
+  // By the batch's average, as the host knows no more. The kernel for few rows takes up to 16
+  // rows per sequence and head (64 sequences of one token, 4 heads to one: bf16 204 us against
+  // 264 in tiles of 128 rows, e4m3 123 against 331), and up to 32 where there are many
+  // sequences (32 of 6 tokens: on 500 positions bf16 24 us against 30, e4m3 29 against 32; on
+  // 4000 e4m3 84 against 110, but bf16 127 against 112). With fewer, each is cut into many
+  // parts, whose records of 32 rows cost more than half-empty tiles (8 sequences on 4000: bf16
+  // 48 us against 33, e4m3 47 against 37), except for e4m3 heads of 256, which the kernel
+  // for many rows is slow at (81 us against 102, runs of 32 99 against 146; on 500 positions
+  // 38 against 32). Beyond 32 rows it loses (32 sequences of 16 tokens on 4000: bf16 186 us
+  // against 117, e4m3 134 against 114). A few long chunks among many single tokens go by the
+  // average too: 256 tokens on 1000 and a chunk of 512 after 8000, bf16 863 us, 281 us as two calls.
   const int mt = rows > 16LL * p.batch ? 2 : 1;
   const bool few = mt == 1 || (rows <= 32LL * p.batch && (4LL * p.batch * p.hkv > p.num_cus || (p.fp8 && p.d > 128)));
   set_shape(p, few ? 16 * mt : 128, few ? kRowsStep : kTileStep);

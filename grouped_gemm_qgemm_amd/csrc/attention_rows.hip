@@ -14,11 +14,12 @@
 // and remainder): the result is that of fp32 probabilities, rounded once.
 //
 // Measured (heads of 128, 32 on 8, pages of 128): 64 sequences with 1 to 8192
-// positions, 207 us on bf16 (5.4 TB/s of cache read; a copy reaches 5.1 TB/s read and
-// written, a contiguous read 6.2) and 125 us on e4m3 (4.6 TB/s). The same without the
-// arithmetic takes as long: what counts is how the cache is read. One head per
+// positions, 204 us on bf16 (5.4 TB/s of cache read; a contiguous read reaches 6.2) and
+// 124 us on e4m3 (4.6 TB/s), runs of 32 147 us; heads of 256 (16 on 4) 220 us. The same
+// without the arithmetic takes as long: what counts is how the cache is read. One head per
 // workgroup, 256 or 128 bytes of each cache row: 222 and 141 us; rings of three or
-// four blocks with the waves that fit then: 226 and 255, 146 and 144.
+// four blocks with the waves that fit then: 226 and 255, 146 and 144 (when those 204 and
+// 124 were 207 and 125).
 //
 // Running maximum, e4m3 scales and what a row must not see are dealt with as in
 // the kernel for many rows.

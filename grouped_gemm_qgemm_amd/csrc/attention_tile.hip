@@ -25,17 +25,18 @@
 // are fp32. The one rounding inside is that of the probabilities to bf16, which
 // the MFMA takes (at most 2^-8 of each, as the output's own rounding).
 //
-// Measured (heads of 128, 32 on 8): a prompt of 8192 in 566 us, 971 TFLOP/s over the
-// pairs that see each other; 1000 tokens after a history of 32000 in 549 us, 970 TFLOP/s
-// (a large bf16 library product: 1.15 to 1.2 PFLOP/s); eight prompts of 1 to 1024 tokens
-// 43 us. 64 rows per wave, which would halve the LDS reads, leaves one wave per SIMD
+// Measured (heads of 128, 32 on 8): a prompt of 8192 in 528 us, 1041 TFLOP/s over the
+// pairs that see each other; 1000 tokens after a history of 32000 in 512 us, 1039 TFLOP/s
+// (a large bf16 library product: 1.15 to 1.22 PFLOP/s); eight prompts of 1 to 1024 tokens
+// 42 us. 64 rows per wave, which would halve the LDS reads, leaves one wave per SIMD
 // and accumulators that the compiler moves in and out of AGPRs: 280 TFLOP/s.
-// e4m3 caches reach 590 TFLOP/s (0.27 ms for eight chunks of 1 to 1024 tokens on up to
-// 4096; runs of 64 0.33 ms, of 32 0.41): MFMA busy 24 %, VALU 35 %, the rest is the wait
-// for a block's codes between its loads and its conversion. Page numbers looked up a
-// block ahead did not shorten it (0.30 ms). Heads of 256 reach 438 TFLOP/s: 128
-// accumulators and 64 query registers leave one wave per SIMD, and nothing covers
-// its LDS latencies (a ring of four blocks: 324 -> 355 us).
+// e4m3 caches reach 604 TFLOP/s (0.26 ms for eight chunks of 1 to 1024 tokens on up to
+// 4096; runs of 64 0.32 ms, of 32 0.41): MFMA busy 25 %, VALU 36 %; codes wait in registers
+// between a block's loads and its conversion, and a quarter of the time passes with
+// workgroups that have ended (uncut tiles of unequal length). Page numbers looked up a
+// block ahead did not shorten it (0.30 ms). Heads of 256 reach 449 TFLOP/s (e4m3 chunks
+// 0.81 ms, runs of 64 1.04, of 32 1.27): 128 accumulators and 64 query registers leave
+// one wave per SIMD, and nothing covers its LDS latencies (a ring of four blocks: 324 -> 355 us).
 //
 // A position that a row must not see takes a score of -infinity by selection.
 // Its value row is still multiplied, by zero: where it holds an infinity or NaN

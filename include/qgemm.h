@@ -427,11 +427,15 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
  *                     meaning; calls that may run at the same time each need their own
  *
  * D is a multiple of 8 (QG_ERR_ALIGN), at most 256 (QG_ERR_UNSUPPORTED). Every
- * token sees itself, so no row is empty. What a row must not see does not reach
- * it, infinities and NaN included; pages (page table entries) that no token of
- * the call sees are not read. Scores, softmax statistics and sums are fp32; the
- * probabilities are rounded to bf16 for their product with the values, and the
- * result to bf16 (nearest-even). The result does not depend on timing: the same
+ * token sees itself, so no row is empty. What a row must not see does not reach it,
+ * infinities and NaN included: it changes no bit of the row. Among the values that
+ * it sees, an infinity or NaN counts however small its weight, and the mean of
+ * finite values is as accurate near the end of the type's range as elsewhere. Pages
+ * (page table entries) that no token of the call sees are not read. Scores, softmax
+ * statistics and sums are fp32 (scores beyond its range have no softmax); the
+ * probabilities, times a value's scale, are rounded to bf16 for their product with
+ * the values (with few rows per sequence to two of them, value and remainder), and
+ * the result to bf16 (nearest-even). The result does not depend on timing: the same
  * call gives the same bits. Offsets, lengths and page ids are not re-validated on
  * the device. Sizes that 32 bits do not count, or that need 2^24 workgroups or more
  * (T * Hq / 128 + B * Hkv in the order of 2^24), are QG_ERR_UNSUPPORTED.
