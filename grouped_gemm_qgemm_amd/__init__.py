@@ -25,9 +25,21 @@ Entry points (same names as the C ABI):
     kv_matmul_ragged_paged_scale(... the same, weight = [W_k | W_v] ...)
     tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_lengths,
                         new_lengths, free_pages, free_count, page_size)
+    release_ragged_paged(free_pages, result, page_table, held_lengths, kept_lengths, free_count,
+                         page_size)
+    rope_ragged_paged(q_out, q, k, v, input_row_offsets, kv_blocks, cache_lengths, page_table,
+                      layer_idx, inv_freq, positions=None, interleaved=False, amplitude=1.0,
+                      kv_scales=None, quantization_granularity=0)
+    kv_read_ragged_paged(k_out, v_out, output_row_offsets, first_positions, kv_blocks, page_table,
+                         layer_idx, kv_scales=None, quantization_granularity=0)
+    kv_keep_ragged_paged(path, kept, kv_blocks, cache_lengths, page_table, kv_scales=None,
+                         quantization_granularity=0)
     attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, page_table,
                            layer_idx, scale, workspace, causal=True, window=0,
                            kv_scales=None, quantization_granularity=0)
+    attention_tree_ragged_paged(out, q, input_row_offsets, tree_mask, kv_blocks, cache_lengths,
+                                page_table, layer_idx, scale, workspace, window=0,
+                                kv_scales=None, quantization_granularity=0)
     attention_ragged_paged_workspace(T, batch, num_q_heads, num_kv_heads, head_dim)
 Each returns None on success and raises QgError carrying the status otherwise.
 Measurement yardsticks (include/qgemm_probe.h): read_contiguous, read_strips, mfma_loop,
@@ -44,7 +56,9 @@ import torch
 __all__ = ["load", "QgError", "qgemm_w4", "qgemm_w4_nk", "qgemm_w4_epilogue", "grouped_gemm", "grouped_gemm_w4",
            "grouped_gemm_epilogue", "grouped_gemm_w4_epilogue",
            "k_matmul_ragged_paged_scale", "kv_matmul_ragged_paged_scale",
-           "tables_ragged_paged", "attention_ragged_paged", "attention_ragged_paged_workspace", "status_string", "LIB_PATH", "QG", "EPI_BIAS", "EPI_RESIDUAL",
+           "tables_ragged_paged", "release_ragged_paged", "rope_ragged_paged", "kv_read_ragged_paged",
+           "kv_keep_ragged_paged", "attention_ragged_paged", "attention_tree_ragged_paged",
+           "attention_ragged_paged_workspace", "status_string", "LIB_PATH", "QG", "EPI_BIAS", "EPI_RESIDUAL",
            "EPI_SILU_GATE"]
 
 # qgemm_w4_epilogue flags
@@ -126,6 +140,16 @@ def load(path: str | None = None):
     lib.attention_ragged_paged.argtypes = [V, V, V, V, ctypes.c_uint32, ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
                                            V, V]
     lib.attention_ragged_paged.restype = ctypes.c_int
+    lib.release_ragged_paged.argtypes = [V, V, V, V, V, V, ctypes.c_int32, V]
+    lib.release_ragged_paged.restype = ctypes.c_int
+    lib.rope_ragged_paged.argtypes = [V, V, V, V, V, V, V, ctypes.c_uint32, V, V, ctypes.c_int32, ctypes.c_float, V]
+    lib.rope_ragged_paged.restype = ctypes.c_int
+    lib.kv_read_ragged_paged.argtypes = [V, V, V, V, V, ctypes.c_uint32, V]
+    lib.kv_read_ragged_paged.restype = ctypes.c_int
+    lib.kv_keep_ragged_paged.argtypes = [V, V, V, V]
+    lib.kv_keep_ragged_paged.restype = ctypes.c_int
+    lib.attention_tree_ragged_paged.argtypes = [V, V, V, V, V, ctypes.c_uint32, ctypes.c_float, ctypes.c_int32, V, V]
+    lib.attention_tree_ragged_paged.restype = ctypes.c_int
     lib.attention_ragged_paged_workspace.argtypes = [ctypes.c_int64] * 5
     lib.attention_ragged_paged_workspace.restype = ctypes.c_int64
     lib.qg_status_string.argtypes = [ctypes.c_int]
@@ -407,6 +431,32 @@ def _launch(fn, dev, stream, *args) -> int:
         return fn(*args, s)
 
 
+def _rows_batch(row_offsets) -> int:
+    """Sequences that [B + 1] row offsets are of; -1 where that cannot be told."""
+    return row_offsets.shape[0] - 1 if row_offsets is not None and row_offsets.dim() == 1 else -1
+
+
+def _cache_record(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity, batch: int):
+    """The bytes of a qg_paged_kv; None (a NULL descriptor) without blocks."""
+    if kv_blocks is None:
+        return None
+    # the C ABI takes these two by address alone, so their form is checked here
+    pages = 0
+    if page_table is not None:
+        if page_table.dim() != 2 or (batch >= 0 and page_table.shape[0] != batch):
+            raise ValueError("page_table must be [B, max_pages]")
+        pages = page_table.shape[1]
+    if cache_lengths is not None and (cache_lengths.dim() != 1 or (batch >= 0 and cache_lengths.shape[0] != batch)):
+        raise ValueError("cache_lengths must be [B]")
+    for t in (cache_lengths, page_table):
+        if t is not None and (t.dtype not in _TABLE_DTYPE or not t.is_contiguous()):
+            raise ValueError("cache_lengths and page_table must be contiguous int32 or uint32 tensors")
+    return (_record(kv_blocks, _CACHE_DTYPE)
+            + _KV_TABLES(0 if cache_lengths is None else cache_lengths.data_ptr(),
+                         0 if page_table is None else page_table.data_ptr(), pages)
+            + (_NO_TENSOR if kv_scales is None else _record(kv_scales)) + _KV_GRANULARITY(quantization_granularity))
+
+
 def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_lengths, new_lengths, free_pages,
                         free_count, page_size: int, stream=None, raise_on_error: bool = True) -> int:
     """Row offsets [B + 1], new page table entries (page_table [B, W], updated) and slot map
@@ -420,6 +470,92 @@ def tables_ragged_paged(input_row_offsets, slot_map, page_table, result, cache_l
     st = _launch(lib.tables_ragged_paged, dev, stream, _record(input_row_offsets, u32), _record(slot_map),
                  _record(page_table, u32), _record(result, u32), _record(cache_lengths, u32), _record(new_lengths, u32),
                  _record(free_pages, u32), _record(free_count, u32), _int32("page_size", page_size))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def release_ragged_paged(free_pages, result, page_table, held_lengths, kept_lengths, free_count, page_size: int,
+                         stream=None, raise_on_error: bool = True) -> int:
+    """Pages of positions kept_lengths[b] .. held_lengths[b] - 1 ([B], whole pages only) go back on
+    the stack free_pages [F] (updated from free_count [1] on), in the order in which
+    tables_ragged_paged hands them out. result [2]: pages now on the stack, status (0: done; else
+    1 no room on the stack | 2 a sequence past page_table's W pages, nothing written)."""
+    lib = load()
+    dev = _device_of((free_pages, result, page_table, held_lengths, kept_lengths, free_count))
+    u32 = _TABLE_DTYPE
+    st = _launch(lib.release_ragged_paged, dev, stream, _record(free_pages, u32), _record(result, u32),
+                 _record(page_table, u32), _record(held_lengths, u32), _record(kept_lengths, u32),
+                 _record(free_count, u32), _int32("page_size", page_size))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+_ROW_STRIDES = struct.Struct("<qqq").pack
+
+
+def _rows_record(t):
+    """The bytes of a qg_tensor for [T, H, D] whose rows may be parts of longer ones, and the
+    elements from one row to the next."""
+    if t is None:
+        return None, 0
+    if t.dim() != 3:
+        return _RECORD[min(t.dim(), MAX_RANK)](t.data_ptr(), _TORCH_TO_QG.get(t.dtype, -1), t.dim(), *t.shape[:MAX_RANK]), 0
+    (rows, heads, d), (row, head, one) = t.shape, t.stride()
+    if t.numel() and ((d > 1 and one != 1) or (heads > 1 and head != d)):
+        raise ValueError("the heads of a row must be contiguous")
+    return (_RECORD[3](t.data_ptr(), _TORCH_TO_QG.get(t.dtype, -1), 3, rows, heads, d),
+            row if rows > 1 and t.numel() else heads * d)
+
+
+def rope_ragged_paged(q_out, q, k, v, input_row_offsets, kv_blocks, cache_lengths, page_table, layer_idx: int, inv_freq,
+                      positions=None, interleaved: bool = False, amplitude: float = 1.0, kv_scales=None,
+                      quantization_granularity: int = 0, stream=None, raise_on_error: bool = True) -> int:
+    """Rotary positions of the new tokens: q [T, Hq, D] turned into q_out, k [T, Hkv, D] turned and
+    v as it is written into layer `layer_idx` of the paged cache at positions
+    cache_lengths[b] + j (bf16, or quantized to e4m3 with f32 `kv_scales`). q, k and v (bf16) may be
+    views of a fused projection's rows; q and q_out, or k and v, may be None. inv_freq [R / 2]
+    (f32): the first R elements of a head are turned, as pairs R / 2 apart or (interleaved) side by
+    side, by positions[r] (int32; default cache_lengths[b] + j) * inv_freq, times `amplitude`."""
+    lib = load()
+    dev = _device_of((q_out, q, k, v, input_row_offsets, kv_blocks, cache_lengths, page_table, inv_freq, positions, kv_scales))
+    kv = _cache_record(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity, _rows_batch(input_row_offsets))
+    (q_rec, qs), (k_rec, ks), (v_rec, vs) = _rows_record(q), _rows_record(k), _rows_record(v)
+    st = _launch(lib.rope_ragged_paged, dev, stream, _record(q_out), q_rec, k_rec, v_rec, _ROW_STRIDES(qs, ks, vs),
+                 _record(input_row_offsets, _TABLE_DTYPE), kv, _int32("layer_idx", layer_idx, 0xFFFFFFFF), _record(inv_freq),
+                 _record(positions), 1 if interleaved else 0, amplitude)
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def kv_read_ragged_paged(k_out, v_out, output_row_offsets, first_positions, kv_blocks, page_table, layer_idx: int,
+                         kv_scales=None, quantization_granularity: int = 0, stream=None, raise_on_error: bool = True) -> int:
+    """Rows output_row_offsets[b] + j of k_out and v_out [T, Hkv, D] (bf16 or f32; either may be
+    None) become keys and values of position first_positions[b] + j (None: from 0) of layer
+    `layer_idx` of the paged cache, e4m3 codes times their scales."""
+    lib = load()
+    dev = _device_of((k_out, v_out, output_row_offsets, first_positions, kv_blocks, page_table, kv_scales))
+    kv = _cache_record(kv_blocks, None, page_table, kv_scales, quantization_granularity, _rows_batch(output_row_offsets))
+    st = _launch(lib.kv_read_ragged_paged, dev, stream, _record(k_out), _record(v_out),
+                 _record(output_row_offsets, _TABLE_DTYPE), _record(first_positions, _TABLE_DTYPE), kv,
+                 _int32("layer_idx", layer_idx, 0xFFFFFFFF))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def kv_keep_ragged_paged(path, kept, kv_blocks, cache_lengths, page_table, kv_scales=None,
+                         quantization_granularity: int = 0, stream=None, raise_on_error: bool = True) -> int:
+    """In every layer of the paged cache, position cache_lengths[b] + i receives keys and values of
+    position cache_lengths[b] + path[b][i], for i < kept[b]: the accepted tokens of a draft tree
+    moved together. path [B, M] (int32), strictly increasing; kept [B]."""
+    lib = load()
+    dev = _device_of((path, kept, kv_blocks, cache_lengths, page_table, kv_scales))
+    kv = _cache_record(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity,
+                       kept.shape[0] if kept is not None and kept.dim() == 1 else -1)
+    st = _launch(lib.kv_keep_ragged_paged, dev, stream, _record(path), _record(kept, _TABLE_DTYPE), kv)
     if raise_on_error:
         _check(st)
     return st
@@ -441,26 +577,27 @@ def attention_ragged_paged(out, q, input_row_offsets, kv_blocks, cache_lengths, 
     tensor of attention_ragged_paged_workspace(...) elements."""
     lib = load()
     dev = _device_of((out, q, input_row_offsets, kv_blocks, cache_lengths, page_table, kv_scales, workspace))
-    kv = None
-    if kv_blocks is not None:
-        # the C ABI takes these two by address alone, so their form is checked here
-        batch = input_row_offsets.shape[0] - 1 if input_row_offsets is not None and input_row_offsets.dim() == 1 else -1
-        pages = 0
-        if page_table is not None:
-            if page_table.dim() != 2 or (batch >= 0 and page_table.shape[0] != batch):
-                raise ValueError("page_table must be [B, max_pages]")
-            pages = page_table.shape[1]
-        if cache_lengths is not None and (cache_lengths.dim() != 1 or (batch >= 0 and cache_lengths.shape[0] != batch)):
-            raise ValueError("cache_lengths must be [B]")
-        for t in (cache_lengths, page_table):
-            if t is not None and (t.dtype not in _TABLE_DTYPE or not t.is_contiguous()):
-                raise ValueError("cache_lengths and page_table must be contiguous int32 or uint32 tensors")
-        kv = (_record(kv_blocks, _CACHE_DTYPE)
-              + _KV_TABLES(0 if cache_lengths is None else cache_lengths.data_ptr(),
-                           0 if page_table is None else page_table.data_ptr(), pages)
-              + (_NO_TENSOR if kv_scales is None else _record(kv_scales)) + _KV_GRANULARITY(quantization_granularity))
+    kv = _cache_record(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity, _rows_batch(input_row_offsets))
     st = _launch(lib.attention_ragged_paged, dev, stream, _record(out), _record(q), _record(input_row_offsets, _TABLE_DTYPE),
                  kv, _int32("layer_idx", layer_idx, 0xFFFFFFFF), scale, 1 if causal else 0, _int32("window", window), _record(workspace))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def attention_tree_ragged_paged(out, q, input_row_offsets, tree_mask, kv_blocks, cache_lengths, page_table, layer_idx: int,
+                                scale: float, workspace, window: int = 0, kv_scales=None,
+                                quantization_granularity: int = 0, stream=None, raise_on_error: bool = True) -> int:
+    """attention_ragged_paged for drafted tokens that form trees: a token sees its sequence's
+    history and those drafted tokens i whose bit (i % 32 of word i / 32) is set in its row of
+    tree_mask [T, W] (int32 or uint32). window: 0, or the number of positions a token sees, the
+    drafted ones first. A row that sees nothing becomes zeros."""
+    lib = load()
+    dev = _device_of((out, q, input_row_offsets, tree_mask, kv_blocks, cache_lengths, page_table, kv_scales, workspace))
+    kv = _cache_record(kv_blocks, cache_lengths, page_table, kv_scales, quantization_granularity, _rows_batch(input_row_offsets))
+    st = _launch(lib.attention_tree_ragged_paged, dev, stream, _record(out), _record(q), _record(input_row_offsets, _TABLE_DTYPE),
+                 _record(tree_mask, _TABLE_DTYPE), kv, _int32("layer_idx", layer_idx, 0xFFFFFFFF), scale,
+                 _int32("window", window), _record(workspace))
     if raise_on_error:
         _check(st)
     return st

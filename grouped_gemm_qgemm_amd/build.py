@@ -43,6 +43,7 @@ COMMON = [
 SOURCE_FLAGS = {
     "w4_decode.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
     "attention_rows.hip": ["-mllvm", "-enable-ipra=0"],
+    "attention_rows_tree.hip": ["-mllvm", "-enable-ipra=0"],
 }
 
 

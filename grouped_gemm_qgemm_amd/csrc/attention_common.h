@@ -158,7 +158,12 @@ __device__ __forceinline__ int over_group(const AttnArgs& p, int x) { return (in
 // Tiles of a sequence, and the positions its longest tile may cover (window_span: the
 // window and what a tile's tokens and the rounding of its start add to it).
 __device__ __forceinline__ int attn_tiles(const AttnArgs& p, int fresh) { return (fresh * p.group + p.bm - 1) >> p.bm_log2; }
-__device__ __forceinline__ int attn_span(const AttnArgs& p, int len) { return p.window ? min(len, p.window_span) : len; }
+// In a tree every tile may see all drafted tokens, and up to `window` positions before them.
+template <bool TREE>
+__device__ __forceinline__ int attn_span(const AttnArgs& p, int len, int fresh) {
+  if (TREE) return p.window ? (int)min((unsigned)len, (unsigned)p.window + (unsigned)fresh + (unsigned)p.step) : len;
+  return p.window ? min(len, p.window_span) : len;
+}
 
 template <int NT>
 struct AttnScan {
@@ -179,7 +184,7 @@ __device__ __forceinline__ int attn_chunks(int span, int chunk) { return span <=
 // Item `want` of each head; all NT threads call it. Items are ordered
 // by sequence, then chunk, then tile (the last tiles, which see the most positions,
 // first). Workgroup 0 also writes the workspace's count of records.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (p.batch <= 64) {
@@ -191,7 +196,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
       fresh = (int)p.offs[lane + 1] - row0;
       len = fresh + (int)p.cache_len[lane];
     }
-    const int tiles = attn_tiles(p, fresh), span = attn_span(p, len);
+    const int tiles = attn_tiles(p, fresh), span = attn_span<TREE>(p, len, fresh);
     unsigned long long all = lane < p.batch ? (unsigned long long)tiles * (unsigned)span : 0;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
@@ -239,7 +244,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
       if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
-      cost += (unsigned long long)attn_tiles(p, fresh) * (unsigned)attn_span(p, len);
+      cost += (unsigned long long)attn_tiles(p, fresh) * (unsigned)attn_span<TREE>(p, len, fresh);
     }
   }
 #pragma unroll
@@ -263,7 +268,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
         len = fresh + (int)p.cache_len[b];
       }
       tiles = attn_tiles(p, fresh);
-      if (tiles) ns = attn_chunks(attn_span(p, len), chunk);
+      if (tiles) ns = attn_chunks(attn_span<TREE>(p, len, fresh), chunk);
     }
     const int items = tiles * ns, cuts = ns > 1 ? tiles : 0, slots = cuts * ns * p.hkv;
     int ii = items, is = slots, ic = cuts;
@@ -303,16 +308,50 @@ struct AttnTile {
   int start;              // begin rounded down
 };
 
+// Drafted tokens of a sequence that its rows of the mask have a bit for.
+__device__ __forceinline__ int tree_named(const AttnArgs& p, int fresh) { return min(fresh, 32 * p.tree_words); }
+
+template <bool TREE>
 __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& p, const AttnItem& it) {
   AttnTile t;
   t.r_first = it.tile << p.bm_log2;
   t.r_count = min(it.fresh * p.group - t.r_first, p.bm);
   t.t_first = over_group(p, t.r_first);
   t.t_last = over_group(p, t.r_first + t.r_count - 1);
-  t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
-  t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
+  if (TREE) {
+    t.end = it.cached + tree_named(p, it.fresh);
+    t.begin = p.window ? max(0, it.cached - p.window) : 0;
+  } else {
+    t.end = p.causal ? it.cached + t.t_last + 1 : it.cached + it.fresh;
+    t.begin = p.window ? max(0, it.cached + t.t_first - p.window + 1) : 0;
+  }
   t.start = t.begin & -p.step;   // so that the first unit, or chunk, holds a position that is seen (step: a power of two)
   return t;
+}
+
+// The low n bits, n clamped to 0 .. 32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
+
+// First position of the history that token `tok` of a tree sees.
+__device__ __forceinline__ int tree_low(const AttnArgs& p, const AttnItem& it, int tok) {
+  if (!p.window) return 0;
+  const uint32_t* words = p.tree + (size_t)(it.row0 + tok) * p.tree_words;
+  const int n = tree_named(p, it.fresh);
+  int seen = 0;
+  for (int w = 0; 32 * w < n; ++w) seen += __popc(words[w] & low_bits(n - 32 * w));
+  return max(0, it.cached - max(p.window - seen, 0));
+}
+
+// Bit i: whether token `tok` of a tree, whose history begins at `lo`, sees position k0 + i,
+// for positions below `end`.
+__device__ __forceinline__ uint32_t tree_sees(const AttnArgs& p, const AttnItem& it, int tok, int lo, int k0, int end) {
+  const uint32_t* words = p.tree + (size_t)(it.row0 + tok) * p.tree_words;
+  const int at = k0 - it.cached, w = at >> 5, most = p.tree_words - 1;   // bit 0 is drafted token `at`
+  const uint32_t x = words[min(max(w, 0), most)], y = words[min(max(w + 1, 0), most)];
+  const uint64_t both = (uint64_t)(w >= 0 && w <= most ? x : 0u) | (uint64_t)(w + 1 >= 0 && w < most ? y : 0u) << 32;
+  const uint32_t drafted = (uint32_t)(both >> (at & 31)) & ~low_bits(-at) & low_bits(min(tree_named(p, it.fresh), end - it.cached) - at);
+  const uint32_t history = low_bits(min(it.cached, end) - k0) & ~low_bits(lo - k0);
+  return drafted | history;
 }
 
 // The line's cut into `pieces` shares: the first `extra` have one unit more than `each`.
@@ -335,7 +374,10 @@ struct AttnShare {
   int row0, fresh, cached;    // of sequence b
 };
 // units of each tile of a sequence
-__device__ __forceinline__ int attn_units(const AttnArgs& p, int len) { return (attn_span(p, len) + p.step - 1) >> p.step_log2; }
+template <bool TREE>
+__device__ __forceinline__ int attn_units(const AttnArgs& p, int len, int fresh) {
+  return (attn_span<TREE>(p, len, fresh) + p.step - 1) >> p.step_log2;
+}
 
 template <int NT>
 struct ShareScan {
@@ -345,7 +387,7 @@ struct ShareScan {
 
 // Workgroups go to the eight XCDs in turn: all heads of a piece to one of them, so that
 // its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
-template <int NT>
+template <int NT, bool TREE>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const bool one_wave = p.batch <= 64;   // every wave looks at all sequences, one per lane: no barrier
@@ -358,7 +400,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
     if (b < p.batch) {
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
-      const uint32_t units = (uint32_t)(attn_tiles(p, fresh) * attn_units(p, len));
+      const uint32_t units = (uint32_t)(attn_tiles(p, fresh) * attn_units<TREE>(p, len, fresh));
       if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; units0 = units; }
       all += units;
     }
@@ -413,14 +455,14 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
     s.row0 = __builtin_amdgcn_readlane(row00, at);
     s.fresh = __builtin_amdgcn_readlane(fresh0, at);
     s.cached = __builtin_amdgcn_readlane(len0, at) - s.fresh;
-    const uint32_t un = attn_units(p, s.fresh + s.cached);
+    const uint32_t un = attn_units<TREE>(p, s.fresh + s.cached, s.fresh);
     s.tile = local < un ? 0 : local / un;
     s.in_tile = local - s.tile * un;
     return s;
   }
   auto look = [&](int b, uint32_t first, uint32_t units, int row0, int fresh, int len) {
     if (s.at >= first && s.at - first < units) {
-      const uint32_t un = attn_units(p, len), local = s.at - first;
+      const uint32_t un = attn_units<TREE>(p, len, fresh), local = s.at - first;
       sh.found.b = b;
       sh.found.tile = local / un;
       sh.found.in_tile = local % un;
@@ -442,7 +484,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
         row0 = (int)p.offs[b];
         fresh = (int)p.offs[b + 1] - row0;
         len = fresh + (int)p.cache_len[b];
-        units = (uint32_t)(attn_tiles(p, fresh) * attn_units(p, len));
+        units = (uint32_t)(attn_tiles(p, fresh) * attn_units<TREE>(p, len, fresh));
       }
       uint32_t run = units;
 #pragma unroll
@@ -585,6 +627,8 @@ __device__ __forceinline__ Row16 rows_of16(const AttnArgs& p, page_list_t pages,
 // and `hw`, the heads per workgroup.
 void attention_rows_shape(AttnArgs& p, int mt);
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
+hipError_t launch_attention_rows_tree(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
+hipError_t launch_attention_tiles_tree(const AttnArgs& p, unsigned grid, hipStream_t stream);
 
 }  // namespace qg

@@ -102,7 +102,7 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int part
     };
     join(std::false_type{});
     if (__any(!(fabsf(o[0]) + fabsf(o[1]) + fabsf(o[2]) + fabsf(o[3]) < INFINITY))) join(std::true_type{});
-    const float inv = 1.f / sum;
+    const float inv = p.tree && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
     const int row = t.r_first + r, token = over_group(p, row);
     uint16_t* to = p.out + ((size_t)(t.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
     if (phase == 0 && d < p.d)
@@ -189,7 +189,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const long long narrow = std::min<long long>(std::max(p.target / p.hkv, 1), tiles * units);
     const long long grid = std::max((wide + 7) / 8 * 8 * groups, (narrow + 7) / 8 * 8 * p.hkv);
     if (grid > kMostWorkgroups) return hipErrorNotSupported;
-    const hipError_t e = launch_attention_rows(p, mt, (unsigned)grid, stream);
+    const hipError_t e = (p.tree ? launch_attention_rows_tree : launch_attention_rows)(p, mt, (unsigned)grid, stream);
     const long long pieces = std::max(wide, narrow);
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
   }
@@ -202,7 +202,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   const long long chunks = (room + p.min_chunk - 1) / p.min_chunk;
   const long long items = std::min(tiles + p.target / p.hkv + 1, chunks < tiles + p.target ? tiles * chunks : (long long)INT64_MAX);
   if (items > kMostWorkgroups / p.hkv) return hipErrorNotSupported;
-  const hipError_t e = launch_attention_tiles(p, (unsigned)(items * p.hkv), stream);
+  const hipError_t e = (p.tree ? launch_attention_tiles_tree : launch_attention_tiles)(p, (unsigned)(items * p.hkv), stream);
   // tiles that are cut have at least two slots each, of fewer than 2 target
   return e != hipSuccess || chunks <= 1 ? e : launch_join(p, std::min(tiles, (long long)(p.target / p.hkv + 1)), stream);
 }

@@ -428,16 +428,195 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
   return launch_status(qg::launch_tables_ragged(p, stream));
 }
 
+qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* result, const qg_tensor* page_table,
+                               const qg_tensor* held_lengths, const qg_tensor* kept_lengths,
+                               const qg_tensor* free_count, int32_t page_size, hipStream_t stream) {
+  if (!free_pages || !result || !page_table || !held_lengths || !kept_lengths || !free_count) return QG_ERR_NULL;
+  qg_status st;
+  if ((st = check_tensor(free_pages, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(result, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(page_table, 2, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(held_lengths, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(kept_lengths, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(free_count, 1, QG_U32)) != QG_OK) return st;
+  const int64_t B = held_lengths->shape[0], W = page_table->shape[1], F = free_pages->shape[0];
+  if (kept_lengths->shape[0] != B || page_table->shape[0] != B) return QG_ERR_SHAPE;
+  if (result->shape[0] != 2 || free_count->shape[0] != 1) return QG_ERR_SHAPE;
+  if (page_size <= 0) return QG_ERR_INVALID_ARG;
+  if (B > qg::kTablesMaxBatch || W >= INT32_MAX / page_size || F > INT32_MAX) return QG_ERR_UNSUPPORTED;
+  if (B == 0) return QG_OK;
+  qg::ReleaseArgs p{static_cast<uint32_t*>(free_pages->data), static_cast<uint32_t*>(result->data),
+                    static_cast<const uint32_t*>(page_table->data), static_cast<const uint32_t*>(held_lengths->data),
+                    static_cast<const uint32_t*>(kept_lengths->data), static_cast<const uint32_t*>(free_count->data),
+                    (int)B, (int)W, F, page_size, device_cus()};
+  return launch_status(qg::launch_release_ragged(p, stream));
+}
+
+// The cache of a call for B sequences: its form first, then, where rows are to be moved,
+// what they are reached by.
+static qg_status check_cache(const qg_paged_kv* kv) {
+  if (kv->blocks.rank != 6) return QG_ERR_RANK;
+  const bool fp8 = kv->blocks.dtype == QG_FP8_E4M3;
+  qg_status st;
+  if ((st = check_tensor(&kv->blocks, 6, fp8 ? QG_FP8_E4M3 : QG_BF16)) != QG_OK) return st;
+  if (kv->blocks.shape[1] != 2) return QG_ERR_SHAPE;
+  if (kv->blocks.shape[5] % 8 != 0) return QG_ERR_ALIGN;
+  return fp8 ? check_cache_scales(kv) : QG_OK;
+}
+static qg_status cache_args(const qg_paged_kv* kv, int64_t B, bool lengths, qg::CacheArgs* out) {
+  const int64_t* bs = kv->blocks.shape;
+  if (bs[2] == 0 || bs[3] == 0 || kv->max_pages_per_seq <= 0) return QG_ERR_INVALID_ARG;
+  if ((lengths && !kv->cache_lengths) || !kv->page_table) return QG_ERR_NULL;
+  // positions of a sequence are counted in 32 bits
+  if (B > INT32_MAX / 2 || bs[3] > INT32_MAX / 2 || kv->max_pages_per_seq > (INT32_MAX / 2) / bs[3]) return QG_ERR_UNSUPPORTED;
+  if (bs[4] > (1 << 26) / bs[5]) return QG_ERR_UNSUPPORTED;   // a cache row's bytes too
+  const bool fp8 = kv->blocks.dtype == QG_FP8_E4M3;
+  out->blocks = kv->blocks.data;
+  out->scales = fp8 ? static_cast<float*>(kv->scales.data) : nullptr;
+  out->cache_len = kv->cache_lengths;
+  out->page_table = kv->page_table;
+  out->layers = bs[0];
+  out->pages = bs[2];
+  out->max_pages = kv->max_pages_per_seq;
+  out->batch = (int)B;
+  out->page_size = (int)bs[3];
+  out->hkv = (int)bs[4];
+  out->d = (int)bs[5];
+  out->gran = fp8 ? (int)kv->quantization_granularity : 0;
+  out->fp8 = fp8 ? 1 : 0;
+  return QG_OK;
+}
+constexpr int64_t kMostRows = 1 << 25;   // tokens or rows of a call: a launch has less than 2^32 threads
+
+// One of rope_ragged_paged's inputs [T, H, D], whose rows are `stride` elements apart.
+static qg_status check_rows(const qg_tensor* t, int64_t T, int64_t H, int64_t D, int64_t stride) {
+  if (t->shape[0] != T || t->shape[1] != H || t->shape[2] != D) return QG_ERR_SHAPE;
+  if (stride < H * D) return QG_ERR_SHAPE;
+  return stride % 8 == 0 ? QG_OK : QG_ERR_ALIGN;
+}
+
+qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg_tensor* k, const qg_tensor* v,
+                            const int64_t* row_strides_host, const qg_tensor* input_row_offsets,
+                            const qg_paged_kv* kv, uint32_t layer_idx, const qg_tensor* inv_freq,
+                            const qg_tensor* positions, int32_t interleaved, float amplitude, hipStream_t stream) {
+  if ((!q && !k) || !q != !q_out || !k != !v || !input_row_offsets || !kv || !inv_freq) return QG_ERR_NULL;
+  qg_status st;
+  for (const qg_tensor* t : {q_out, q, k, v})
+    if (t && (st = check_tensor(t, 3, QG_BF16)) != QG_OK) return st;
+  if ((st = check_tensor(input_row_offsets, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_tensor(inv_freq, 1, QG_F32)) != QG_OK) return st;
+  if (positions && (st = check_tensor(positions, 1, QG_I32)) != QG_OK) return st;
+  if ((st = check_cache(kv)) != QG_OK) return st;
+  const int64_t* bs = kv->blocks.shape;
+  const int64_t T = (q ? q : k)->shape[0], Hq = q ? q->shape[1] : 0, Hkv = bs[4], D = bs[5];
+  const int64_t B = input_row_offsets->shape[0] - 1;
+  if (B < 0) return QG_ERR_SHAPE;
+  const int64_t qs = row_strides_host && q ? row_strides_host[0] : Hq * D;
+  const int64_t ks = row_strides_host && k ? row_strides_host[1] : Hkv * D;
+  const int64_t vs = row_strides_host && v ? row_strides_host[2] : Hkv * D;
+  if (q && (st = check_rows(q, T, Hq, D, qs)) != QG_OK) return st;
+  if (q && (st = check_rows(q_out, T, Hq, D, Hq * D)) != QG_OK) return st;
+  if (k && (st = check_rows(k, T, Hkv, D, ks)) != QG_OK) return st;
+  if (k && (st = check_rows(v, T, Hkv, D, vs)) != QG_OK) return st;
+  if (2 * inv_freq->shape[0] > D) return QG_ERR_SHAPE;
+  if (positions && positions->shape[0] != T) return QG_ERR_SHAPE;
+  if ((int64_t)layer_idx >= bs[0]) return QG_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return QG_ERR_INVALID_ARG;
+  if (D > 1024 || T > kMostRows || Hq > (1 << 26) / (D > 0 ? D : 1)) return QG_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0 || D == 0 || (Hq == 0 && (!k || Hkv == 0))) return QG_OK;
+  qg::RopeArgs p{};
+  if ((st = cache_args(kv, B, true, &p.kv)) != QG_OK) return st;
+  if (q && Hq > 0) {
+    p.q_out = static_cast<uint16_t*>(q_out->data);
+    p.q = static_cast<const uint16_t*>(q->data);
+  }
+  if (k && Hkv > 0) {
+    p.k = static_cast<const uint16_t*>(k->data);
+    p.v = static_cast<const uint16_t*>(v->data);
+  }
+  p.q_stride = qs;
+  p.k_stride = ks;
+  p.v_stride = vs;
+  p.offs = static_cast<const uint32_t*>(input_row_offsets->data);
+  p.inv_freq = static_cast<const float*>(inv_freq->data);
+  p.positions = positions ? static_cast<const int32_t*>(positions->data) : nullptr;
+  p.T = T;
+  p.hq = (int)Hq;
+  p.layer = (int)layer_idx;
+  p.half = (int)inv_freq->shape[0];
+  p.interleaved = interleaved ? 1 : 0;
+  p.num_cus = device_cus();
+  p.amplitude = amplitude;
+  return launch_status(qg::launch_rope_paged(p, stream));
+}
+
+qg_status kv_read_ragged_paged(const qg_tensor* k_out, const qg_tensor* v_out, const qg_tensor* output_row_offsets,
+                               const qg_tensor* first_positions, const qg_paged_kv* kv, uint32_t layer_idx,
+                               hipStream_t stream) {
+  if ((!k_out && !v_out) || !output_row_offsets || !kv) return QG_ERR_NULL;
+  qg_status st;
+  const qg_tensor* one = k_out ? k_out : v_out;
+  const qg_dtype type = one->dtype == QG_F32 ? QG_F32 : QG_BF16;
+  for (const qg_tensor* t : {k_out, v_out})
+    if (t && (st = check_tensor(t, 3, type)) != QG_OK) return st;
+  if ((st = check_tensor(output_row_offsets, 1, QG_U32)) != QG_OK) return st;
+  if (first_positions && (st = check_tensor(first_positions, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_cache(kv)) != QG_OK) return st;
+  const int64_t* bs = kv->blocks.shape;
+  const int64_t T = one->shape[0], Hkv = bs[4], D = bs[5], B = output_row_offsets->shape[0] - 1;
+  if (B < 0) return QG_ERR_SHAPE;
+  for (const qg_tensor* t : {k_out, v_out})
+    if (t && (t->shape[0] != T || t->shape[1] != Hkv || t->shape[2] != D)) return QG_ERR_SHAPE;
+  if (first_positions && first_positions->shape[0] != B) return QG_ERR_SHAPE;
+  if ((int64_t)layer_idx >= bs[0]) return QG_ERR_INVALID_ARG;
+  if (T > kMostRows) return QG_ERR_UNSUPPORTED;
+  if (T == 0 || B == 0 || Hkv == 0 || D == 0) return QG_OK;
+  qg::KvReadArgs p{};
+  if ((st = cache_args(kv, B, false, &p.kv)) != QG_OK) return st;
+  p.out[0] = k_out ? k_out->data : nullptr;
+  p.out[1] = v_out ? v_out->data : nullptr;
+  p.offs = static_cast<const uint32_t*>(output_row_offsets->data);
+  p.first = first_positions ? static_cast<const uint32_t*>(first_positions->data) : nullptr;
+  p.T = T;
+  p.layer = (int)layer_idx;
+  p.f32 = type == QG_F32 ? 1 : 0;
+  p.num_cus = device_cus();
+  return launch_status(qg::launch_kv_read(p, stream));
+}
+
+qg_status kv_keep_ragged_paged(const qg_tensor* path, const qg_tensor* kept, const qg_paged_kv* kv,
+                               hipStream_t stream) {
+  if (!path || !kept || !kv) return QG_ERR_NULL;
+  qg_status st;
+  if ((st = check_tensor(path, 2, QG_I32)) != QG_OK) return st;
+  if ((st = check_tensor(kept, 1, QG_U32)) != QG_OK) return st;
+  if ((st = check_cache(kv)) != QG_OK) return st;
+  const int64_t* bs = kv->blocks.shape;
+  const int64_t B = kept->shape[0], M = path->shape[1];
+  if (path->shape[0] != B) return QG_ERR_SHAPE;
+  if (B > kMostRows / 4 || M > INT32_MAX / 2 || bs[0] > INT32_MAX / 2) return QG_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0 || bs[0] == 0 || bs[4] == 0 || bs[5] == 0) return QG_OK;
+  qg::KvKeepArgs p{};
+  if ((st = cache_args(kv, B, true, &p.kv)) != QG_OK) return st;
+  p.path = static_cast<const int32_t*>(path->data);
+  p.kept = static_cast<const uint32_t*>(kept->data);
+  p.width = M;
+  p.num_cus = device_cus();
+  return launch_status(qg::launch_kv_keep(p, stream));
+}
+
 int64_t attention_ragged_paged_workspace(int64_t T, int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
                                          int64_t head_dim) {
   if (T <= 0 || batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0) return 0;
   return qg::attention_paged_workspace(T, batch, num_q_heads, num_kv_heads, head_dim);
 }
 
-qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
-                                 const qg_paged_kv* kv, uint32_t layer_idx, float scale, int32_t causal,
-                                 int32_t window, const qg_tensor* workspace, hipStream_t stream) {
-  if (!out || !q || !input_row_offsets || !kv || !workspace) return QG_ERR_NULL;
+// tree: with tree_mask (then causal is 0)
+static qg_status attention_impl(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                const qg_tensor* tree_mask, const qg_paged_kv* kv, uint32_t layer_idx, float scale,
+                                int32_t causal, int32_t window, const qg_tensor* workspace, bool tree,
+                                hipStream_t stream) {
+  if (!out || !q || !input_row_offsets || !kv || !workspace || (tree && !tree_mask)) return QG_ERR_NULL;
   if (out->rank != 3 || q->rank != 3 || input_row_offsets->rank != 1 || kv->blocks.rank != 6 || workspace->rank != 1)
     return QG_ERR_RANK;
   qg_status st;
@@ -447,6 +626,7 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   const bool fp8 = kv->blocks.dtype == QG_FP8_E4M3;   // quantized cache
   if ((st = check_tensor(&kv->blocks, 6, fp8 ? QG_FP8_E4M3 : QG_BF16)) != QG_OK) return st;
   if ((st = check_tensor(workspace, 1, QG_F32)) != QG_OK) return st;
+  if (tree && (st = check_tensor(tree_mask, 2, QG_U32)) != QG_OK) return st;
   const int64_t T = q->shape[0], Hq = q->shape[1], D = q->shape[2];
   const int64_t B = input_row_offsets->shape[0] - 1;
   const int64_t* bs = kv->blocks.shape;
@@ -454,12 +634,13 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   if (B < 0 || out->shape[0] != T || out->shape[1] != Hq || out->shape[2] != D) return QG_ERR_SHAPE;
   if (bs[1] != 2 || bs[5] != D) return QG_ERR_SHAPE;
   if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0) return QG_ERR_SHAPE;
+  if (tree && (tree_mask->shape[0] != T || tree_mask->shape[1] < 1)) return QG_ERR_SHAPE;
   if (D % 8 != 0) return QG_ERR_ALIGN;
   if (fp8 && (st = check_cache_scales(kv)) != QG_OK) return st;
   if ((int64_t)layer_idx >= L) return QG_ERR_INVALID_ARG;
   // (log2 e: the kernels' exponents have base 2)
   if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f) || window < 0) return QG_ERR_INVALID_ARG;
-  if (window > 0 && !causal) return QG_ERR_UNSUPPORTED;
+  if (window > 0 && !causal && !tree) return QG_ERR_UNSUPPORTED;
   if (D > 256) return QG_ERR_UNSUPPORTED;
   if (T == 0 || B == 0 || Hq == 0 || D == 0) return QG_OK;
   if (P == 0 || S == 0 || kv->max_pages_per_seq <= 0) return QG_ERR_INVALID_ARG;
@@ -469,6 +650,7 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   if (B > INT32_MAX / 2 || S > INT32_MAX / 2 || Hq > INT32_MAX / 2 || T > (INT32_MAX / 2) / (Hq / Hkv) ||
       kv->max_pages_per_seq > (INT32_MAX / 2) / S)
     return QG_ERR_UNSUPPORTED;
+  if (tree && tree_mask->shape[1] > (1 << 24)) return QG_ERR_UNSUPPORTED;   // a row's bits are counted in 32 bits
   if (Hkv > (1 << 26) / D) return QG_ERR_UNSUPPORTED;   // offsets within 16 cache rows are 32-bit
   qg::AttnArgs p{};
   p.out = static_cast<uint16_t*>(out->data);
@@ -495,7 +677,23 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
   p.fp8 = fp8 ? 1 : 0;
   p.num_cus = device_cus();
   p.scale = scale;
+  if (tree) {
+    p.tree = static_cast<const uint32_t*>(tree_mask->data);
+    p.tree_words = (int)tree_mask->shape[1];
+  }
   return launch_status(qg::launch_attention_paged(p, stream));
+}
+
+qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                 const qg_paged_kv* kv, uint32_t layer_idx, float scale, int32_t causal,
+                                 int32_t window, const qg_tensor* workspace, hipStream_t stream) {
+  return attention_impl(out, q, input_row_offsets, nullptr, kv, layer_idx, scale, causal, window, workspace, false, stream);
+}
+
+qg_status attention_tree_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                      const qg_tensor* tree_mask, const qg_paged_kv* kv, uint32_t layer_idx,
+                                      float scale, int32_t window, const qg_tensor* workspace, hipStream_t stream) {
+  return attention_impl(out, q, input_row_offsets, tree_mask, kv, layer_idx, scale, 0, window, workspace, true, stream);
 }
 
 }  // extern "C"

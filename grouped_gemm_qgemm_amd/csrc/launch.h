@@ -106,7 +106,65 @@ struct TablesArgs {
   int num_cus;
 };
 
-// Attention over the paged cache (attention_ragged_paged).
+// Pages back on the free stack (release_ragged_paged).
+struct ReleaseArgs {
+  uint32_t* free_pages;        // [free_len]
+  uint32_t* result;            // [2]
+  const uint32_t* table;       // [batch, max_pages]
+  const uint32_t* held;        // [batch]
+  const uint32_t* kept;        // [batch]
+  const uint32_t* free_count;  // [1]
+  int batch, max_pages;
+  int64_t free_len;
+  int page_size;
+  int num_cus;
+};
+
+// A paged cache as the calls that move its rows take it.
+struct CacheArgs {
+  void* blocks;                // bf16 or e4m3 [L, 2, P, S, Hkv, D]
+  float* scales;               // e4m3: [L, 2, P, S, Hkv, D / gran]
+  const uint32_t* cache_len;   // [batch]
+  const uint32_t* page_table;  // [batch, max_pages]
+  int64_t layers, pages, max_pages;
+  int batch, page_size, hkv, d, gran, fp8;
+  uint32_t div_mul = 0, div_shift = 0;   // the launcher's: page_size as a multiplication
+};
+
+// Rotary positions and the cache's write (rope_ragged_paged).
+struct RopeArgs {
+  CacheArgs kv;
+  uint16_t* q_out;             // bf16 [T, Hq, D] or NULL
+  const uint16_t *q, *k, *v;   // bf16, rows q_stride, k_stride, v_stride elements apart; or NULL
+  int64_t q_stride, k_stride, v_stride;
+  const uint32_t* offs;        // [batch + 1]
+  const float* inv_freq;       // [half]
+  const int32_t* positions;    // [T] or NULL
+  int64_t T;
+  int hq, layer, half, interleaved, num_cus;
+  float amplitude;
+};
+
+// Ranges of the cache as dense rows (kv_read_ragged_paged).
+struct KvReadArgs {
+  CacheArgs kv;
+  void* out[2];                // bf16 or f32 [T, Hkv, D], or NULL
+  const uint32_t* offs;        // [batch + 1]
+  const uint32_t* first;       // [batch] or NULL
+  int64_t T;
+  int layer, f32, num_cus;
+};
+
+// Rows of a path moved together (kv_keep_ragged_paged).
+struct KvKeepArgs {
+  CacheArgs kv;
+  const int32_t* path;         // [batch, width]
+  const uint32_t* kept;        // [batch]
+  int64_t width;
+  int num_cus;
+};
+
+// Attention over the paged cache (attention_ragged_paged, attention_tree_ragged_paged).
 struct AttnArgs {
   uint16_t* out;               // bf16 [T, Hq, D]
   const uint16_t* q;           // bf16 [T, Hq, D]
@@ -124,6 +182,9 @@ struct AttnArgs {
   uint32_t div_mul = 0, div_shift = 0, group_mul = 0, group_shift = 0;
   int bm = 0, bm_log2 = 0, step = 0, step_log2 = 0, window_span = 0;
   int target = 0, target_log2 = 0, min_chunk = 0, hw = 1;
+  // trees of drafted tokens: [T, tree_words], or NULL (then causal and window are as said there)
+  const uint32_t* tree = nullptr;
+  int tree_words = 0;
 };
 
 // Decode-shaped W4A16 (M <= 16).
@@ -140,6 +201,12 @@ hipError_t launch_w4_grouped(const W4GroupedArgs& p, hipStream_t stream);
 hipError_t launch_kproj_fp8(const KProjArgs& p, hipStream_t stream);
 
 hipError_t launch_tables_ragged(const TablesArgs& p, hipStream_t stream);
+
+hipError_t launch_release_ragged(const ReleaseArgs& p, hipStream_t stream);
+
+hipError_t launch_rope_paged(const RopeArgs& p, hipStream_t stream);
+hipError_t launch_kv_read(const KvReadArgs& p, hipStream_t stream);
+hipError_t launch_kv_keep(const KvKeepArgs& p, hipStream_t stream);
 
 hipError_t launch_attention_paged(const AttnArgs& p, hipStream_t stream);
 

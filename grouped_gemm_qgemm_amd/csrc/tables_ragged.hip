@@ -180,17 +180,122 @@ __global__ __launch_bounds__(TT) void tables_ragged_kernel(
   }
 }
 
+// The way back: entries that a sequence no longer needs go onto the stack, with
+//
+//   first_b = sum over the sequences before b of ceil(h / S) - ceil(k / S), R of all
+//   free[count + R - 1 - (first_b + i)] = page_table[b][ceil(k_b / S) + i]
+//
+// so that the kernel above takes the same pages in the same order. One prefix sum,
+// repeated by every workgroup, and independent writes: latency bounds it too.
+__global__ __launch_bounds__(TT) void release_ragged_kernel(
+    uint32_t* __restrict__ free_pages, uint32_t* __restrict__ result, const uint32_t* __restrict__ table,
+    const uint32_t* __restrict__ held, const uint32_t* __restrict__ kept, const uint32_t* __restrict__ free_count,
+    int batch, int max_pages, uint32_t free_len, uint32_t page_size, uint32_t div_mul, uint32_t div_shift) {
+  __shared__ uint32_t s_pg[TSEQ];
+  __shared__ unsigned long long w_pg[TT / 64];
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const uint32_t count = free_count[0];
+  const unsigned long long room = (unsigned long long)max_pages * page_size;   // below 2^31
+  // pages of x positions; x is at most `room` where the result counts
+  auto pages_of = [&](uint32_t x) {
+    const uint32_t y = x + page_size - 1;
+    return (__umulhi(y, div_mul) + y) >> div_shift;
+  };
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int b0 = tid; b0 < batch; b0 += TLD * TT) {
+    uint32_t h[TLD], k[TLD];
+#pragma unroll
+    for (int i = 0; i < TLD; ++i) {
+      const int b = min(b0 + i * TT, batch - 1);
+      h[i] = held[b];
+      k[i] = kept[b];
+    }
+#pragma unroll
+    for (int i = 0; i < TLD; ++i) {
+      uint32_t back = 0;
+      if (k[i] < h[i]) {
+        if (h[i] <= room) {
+          back = pages_of(h[i]) - pages_of(k[i]);
+        } else {   // past what pages_of takes: bad if a page is released at all
+          const unsigned long long more = ((unsigned long long)h[i] + page_size - 1) / page_size -
+                                          ((unsigned long long)k[i] + page_size - 1) / page_size;
+          bad |= more > 0;
+          back = (uint32_t)more;
+        }
+      }
+      if (b0 + i * TT < batch) s_pg[b0 + i * TT] = back;
+    }
+  }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  const int per = (batch + TT - 1) / TT;
+  unsigned long long pg = 0;
+  for (int b = tid * per; b < min(batch, tid * per + per); ++b) pg += s_pg[b];
+  unsigned long long ip = pg;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const unsigned long long v = __shfl_up(ip, d);
+    if (lane >= d) ip += v;
+  }
+  if (lane == 63) w_pg[wave] = ip;
+  __syncthreads();
+  unsigned long long before = 0, pages = 0;
+#pragma unroll
+  for (int w = 0; w < TT / 64; ++w) {
+    if (w < wave) before += w_pg[w];
+    pages += w_pg[w];
+  }
+  unsigned long long at = before + ip - pg;
+  for (int b = tid * per; b < min(batch, tid * per + per); ++b) {
+    const uint32_t back = s_pg[b];
+    s_pg[b] = (uint32_t)at;
+    at += back;
+  }
+  __syncthreads();
+  uint32_t status = 0;
+  if (count > free_len || pages > (unsigned long long)(free_len - count)) status |= 1;
+  if (s_bad) status |= 2;
+  if (blockIdx.x == 0 && tid == 0) {
+    result[0] = status ? count : count + (uint32_t)pages;
+    result[1] = status;
+  }
+  if (status) return;
+  const uint32_t all = (uint32_t)pages, threads = gridDim.x * TT;
+  for (uint32_t j = blockIdx.x * TT + tid; j < all; j += threads) {
+    const int b = owner(s_pg, batch, j);
+    free_pages[count + all - 1 - j] = table[(size_t)b * max_pages + pages_of(kept[b]) + (j - s_pg[b])];
+  }
+}
+
+// x / page_size for x < 2^31 as (umulhi(x, mul) + x) >> shift
+static void divide_by_page(int page_size, uint32_t& mul, uint32_t& shift) {
+  shift = 0;
+  while ((1u << shift) < (uint32_t)page_size) ++shift;
+  mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)page_size)) / (uint64_t)page_size) + 1);
+}
+
 hipError_t launch_tables_ragged(const TablesArgs& p, hipStream_t stream) {
-  // x / page_size for x < 2^31 as (umulhi(x, mul) + x) >> shift
-  uint32_t shift = 0;
-  while ((1u << shift) < (uint32_t)p.page_size) ++shift;
-  const uint32_t mul = (uint32_t)((((1ull << 32) * ((1ull << shift) - (uint64_t)p.page_size)) / (uint64_t)p.page_size) + 1);
+  uint32_t mul, shift;
+  divide_by_page(p.page_size, mul, shift);
   // a workgroup per 2048 tokens (two passes of its threads), at most two per CU (64 KB of LDS)
   const long long want = (p.slot_len + 2 * TTOK * TT - 1) / (2 * TTOK * TT);
   const int grid = (int)(want < 1 ? 1 : want > 2 * p.num_cus ? 2 * p.num_cus : want);
   tables_ragged_kernel<<<grid, TT, 0, stream>>>(p.offsets, p.slots, p.table, p.result, p.cached, p.fresh, p.free_pages,
                                                 p.free_count, p.batch, p.max_pages, (uint32_t)p.free_len, p.slot_len,
                                                 (uint32_t)p.page_size, mul, shift);
+  return hipGetLastError();
+}
+
+hipError_t launch_release_ragged(const ReleaseArgs& p, hipStream_t stream) {
+  uint32_t mul, shift;
+  divide_by_page(p.page_size, mul, shift);
+  // a workgroup per 256 sequences, whose pages only the device knows
+  const int grid = (p.batch + TT - 1) / TT;
+  release_ragged_kernel<<<grid, TT, 0, stream>>>(p.free_pages, p.result, p.table, p.held, p.kept, p.free_count, p.batch,
+                                                 p.max_pages, (uint32_t)p.free_len, (uint32_t)p.page_size, mul, shift);
   return hipGetLastError();
 }
 

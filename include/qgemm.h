@@ -16,11 +16,17 @@
  *   grouped_gemm_w4              the routing of grouped_gemm over experts stored in
  *                                qgemm_w4's packed 4-bit format
  *
- * and two operations around the paged KV cache that the projections fill:
+ * and operations around the paged KV cache that the projections fill:
  *
  *   tables_ragged_paged          row offsets, page table entries and slot map of a step,
  *                                from the sequences' lengths
+ *   release_ragged_paged         pages that sequences no longer need, back on the stack
+ *   rope_ragged_paged            rotary positions of the new tokens' queries and keys;
+ *                                keys and values written (quantized) into the cache
+ *   kv_read_ragged_paged         ranges of the cache read back as dense rows
+ *   kv_keep_ragged_paged         the accepted tokens of a draft tree moved together
  *   attention_ragged_paged       attention of the new tokens over the cache's pages
+ *   attention_tree_ragged_paged  the same for drafted tokens that form trees
  *
  * Conventions shared by every entry point
  *   - Tensor data pointers are DEVICE pointers unless a comment says "host".
@@ -38,7 +44,7 @@
  *     product, returns QG_ERR_UNSUPPORTED.
  *   - Outputs must not alias inputs. Calls on different streams may run
  *     concurrently; the library holds no mutable global state besides a cache of
- *     device properties. attention_ragged_paged's workspace belongs to one call
+ *     device properties. The attention calls' workspace belongs to one call
  *     at a time.
  */
 #ifndef QGEMM_H
@@ -400,6 +406,118 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
                               hipStream_t stream);
 
 /*
+ * release_ragged_paged - pages that sequences no longer need go back on the stack of
+ * free pages: the inverse of tables_ragged_paged, after drafted tokens were rejected or
+ * a sequence ended
+ *
+ * With h_b = held_lengths[b] positions that have pages now, k_b = kept_lengths[b] of
+ * them that stay and S = page_size, entries ceil(k_b / S) .. ceil(h_b / S) - 1 of
+ * sequence b are released (none where k_b >= h_b). R in all, they are written to
+ * free_pages[free_count[0] .. free_count[0] + R - 1], the first of them (in order of b
+ * and then of the entry) on top, so that tables_ragged_paged would hand them out in the
+ * same order again.
+ *
+ *   free_pages        u32 [F]      updated: elements from free_count[0] on; others as they were
+ *   result            u32 [2]      [0]: pages now on the stack, [1]: status (below)
+ *   page_table        u32 [B, W]   read only: released entries keep their (stale) content
+ *   held_lengths, kept_lengths u32 [B]
+ *   free_count        u32 [1]      pages on the stack (result[0] of an earlier call may be it:
+ *                                  a view of its first element, in another buffer)
+ *
+ * result[1] is 0, or the OR of
+ *   1  the stack has no room for the pages (or free_count[0] > F)
+ *   2  a sequence that releases pages holds more than W * S positions
+ * and then nothing but `result` is written, with result[0] = free_count[0]. Page ids are
+ * not checked. B above 8192, or (W + 1) * S above 2^31 - 1, is QG_ERR_UNSUPPORTED; B = 0
+ * is a no-op.
+ */
+qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* result, const qg_tensor* page_table,
+                               const qg_tensor* held_lengths, const qg_tensor* kept_lengths,
+                               const qg_tensor* free_count, int32_t page_size, hipStream_t stream);
+
+/*
+ * rope_ragged_paged - rotary positions of the new tokens' queries and keys; the turned
+ * keys, and the values as they are, are written into layer `layer_idx` of a paged cache
+ *
+ * Token j of sequence b (row r = input_row_offsets[b] + j) has the rotary position
+ * t = positions[r], or cache_lengths[b] + j without `positions` (in a tree of drafted
+ * tokens, a token's depth counts, not its place). With f = inv_freq [R / 2], the first R of
+ * a head's D elements form pairs (x, y): elements (i, i + R / 2), or (2 i, 2 i + 1) when
+ * `interleaved`; pair i becomes
+ *
+ *   (x cos a - y sin a, y cos a + x sin a) * amplitude,    a = t * f[i]
+ *
+ * and elements from R on stay as they are. What slows frequencies for long contexts is
+ * in inv_freq, and in amplitude. The angle is reduced in 64 bits (positions of 31 bits
+ * are served as exactly as small ones), the rest computed in fp32 and rounded once.
+ *
+ *   q_out      bf16 [T, Hq, D]    turned queries
+ *   q          bf16 [T, Hq, D]    or both NULL: no queries
+ *   k, v       bf16 [T, Hkv, D]   or both NULL: nothing is written to the cache
+ *   row_strides_host  HOST int64[3]: elements from one token's row of q, k and v to the
+ *              next (parts of a fused projection's rows), or NULL for dense ones. At least
+ *              H * D (QG_ERR_SHAPE) and a multiple of 8 (QG_ERR_ALIGN)
+ *   input_row_offsets u32 [B + 1] offs[0] = 0, non-decreasing, offs[B] <= T: rows from
+ *              offs[B] on are left as they were
+ *   kv         the cache; key and value of token j of sequence b go to position
+ *              cache_lengths[b] + j: bf16, or quantized as described at qg_paged_kv (from the
+ *              fp32 values). Every other byte is left as it was
+ *   layer_idx  < L (QG_ERR_INVALID_ARG otherwise)
+ *   inv_freq   f32 [R / 2], R <= D (QG_ERR_SHAPE otherwise); R = 0 turns nothing
+ *   positions  i32 [T] or NULL
+ *   amplitude  finite (QG_ERR_INVALID_ARG otherwise)
+ *
+ * D is a multiple of 8 (QG_ERR_ALIGN), at most 1024 (QG_ERR_UNSUPPORTED). One of q and k
+ * at least is given (QG_ERR_NULL). Offsets, lengths and page ids are not re-validated on
+ * the device; two tokens must not address one slot. q_out must not overlap q.
+ */
+qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg_tensor* k, const qg_tensor* v,
+                            const int64_t* row_strides_host, const qg_tensor* input_row_offsets,
+                            const qg_paged_kv* kv, uint32_t layer_idx, const qg_tensor* inv_freq,
+                            const qg_tensor* positions, int32_t interleaved, float amplitude, hipStream_t stream);
+
+/*
+ * kv_read_ragged_paged - ranges of a paged cache read back as dense rows
+ *
+ * Row r = output_row_offsets[b] + j of k_out and v_out becomes the key and value of
+ * position first_positions[b] + j of sequence b: of a bf16 cache as they are, of an e4m3
+ * cache code * scale (fp32, rounded to the output's type).
+ *
+ *   k_out, v_out        bf16 or f32 [T, Hkv, D], both of one type; either may be NULL
+ *   output_row_offsets  u32 [B + 1]   offs[0] = 0, non-decreasing, offs[B] <= T: rows from
+ *                                     offs[B] on are left as they were
+ *   first_positions     u32 [B], or NULL for 0
+ *   kv                  read only; cache_lengths is not used and may be NULL
+ *   layer_idx           < L (QG_ERR_INVALID_ARG otherwise)
+ *
+ * D is a multiple of 8 (QG_ERR_ALIGN). Positions and page ids are not re-validated on the
+ * device; only pages that hold a position of a range are read.
+ */
+qg_status kv_read_ragged_paged(const qg_tensor* k_out, const qg_tensor* v_out, const qg_tensor* output_row_offsets,
+                               const qg_tensor* first_positions, const qg_paged_kv* kv, uint32_t layer_idx,
+                               hipStream_t stream);
+
+/*
+ * kv_keep_ragged_paged - the accepted tokens of each sequence's draft tree moved together
+ *
+ * The drafted tokens of sequence b are at positions cache_lengths[b] + i. For each
+ * i < kept[b], position cache_lengths[b] + i receives keys and values (codes and scales) of
+ * position cache_lengths[b] + path[b][i], in every layer; the content of the positions
+ * behind the kept ones, from cache_lengths[b] + kept[b] to the last of the path, has no meaning
+ * to the caller and stays as it was.
+ *
+ *   path    i32 [B, M]   the kept tokens, strictly increasing: path[b][i] >= i. Entries from
+ *                        kept[b] on are not read as tokens; entries with path[b][i] <= i
+ *                        move nothing
+ *   kept    u32 [B]      at most M (more count as M)
+ *   kv      the cache, updated in place; cache_lengths is not changed
+ *
+ * D is a multiple of 8 (QG_ERR_ALIGN). Positions and page ids are not re-validated on the device.
+ */
+qg_status kv_keep_ragged_paged(const qg_tensor* path, const qg_tensor* kept, const qg_paged_kv* kv,
+                               hipStream_t stream);
+
+/*
  * attention_ragged_paged - attention of each sequence's new tokens over its pages
  * of a paged cache: prompts, chunks of prompts, drafted tokens and single tokens
  * alike, in one ragged call
@@ -445,6 +563,28 @@ int64_t attention_ragged_paged_workspace(int64_t T, int64_t batch, int64_t num_q
 qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
                                  const qg_paged_kv* kv, uint32_t layer_idx, float scale, int32_t causal,
                                  int32_t window, const qg_tensor* workspace, hipStream_t stream);
+
+/*
+ * attention_tree_ragged_paged - attention of drafted tokens that form trees (or any other
+ * order) over their sequences' histories and each other
+ *
+ * As attention_ragged_paged, but for what a token sees: token j of sequence b, of n_b
+ * drafted ones, sees the history, positions 0 .. cache_lengths[b] - 1, and those drafted
+ * tokens i (at position cache_lengths[b] + i) that its row of tree_mask names: bit i % 32 of
+ * tree_mask[input_row_offsets[b] + j][i / 32], for i < min(n_b, 32 W). In a tree these are its
+ * ancestors and itself. A row that sees nothing (no history, no bit) becomes zeros.
+ *
+ *   tree_mask  u32 [T, W], W >= 1 (QG_ERR_SHAPE otherwise); bits from n_b on are ignored
+ *   window     0, or the number of positions a token sees: the drafted ones that the mask names
+ *              and the last max(window - their number, 0) of the history
+ *   workspace  as attention_ragged_paged's, of the same size
+ *
+ * Every other argument, type, check and rule as attention_ragged_paged. More than 2^24
+ * words per row are QG_ERR_UNSUPPORTED.
+ */
+qg_status attention_tree_ragged_paged(const qg_tensor* out, const qg_tensor* q, const qg_tensor* input_row_offsets,
+                                      const qg_tensor* tree_mask, const qg_paged_kv* kv, uint32_t layer_idx,
+                                      float scale, int32_t window, const qg_tensor* workspace, hipStream_t stream);
 
 /* Static, never-NULL text for a status code. */
 const char* qg_status_string(qg_status s);

@@ -25,6 +25,8 @@ from .grouped_w4 import grouped_gemm_w4
 from .kproj import (k_matmul_ragged_paged_scale, kv_matmul_ragged_paged_scale, kproj_exact, kproj_rows,
                     quantize_runs, token_slots)
 from .attention import attention_ragged_paged, cache_rows, tables_ragged_paged
+from .paged import (attention_tree_ragged_paged, kv_keep_ragged_paged, kv_read_ragged_paged, release_ragged_paged, rope,
+                    rope_ragged_paged, tree_mask)
 
 __all__ = [
     "round_to_f16", "round_to_bf16", "round_to", "decode_f16", "decode_bf16", "decode_e4m3",
@@ -33,4 +35,6 @@ __all__ = [
     "grouped_gemm", "grouped_gemm_w4", "k_matmul_ragged_paged_scale", "kv_matmul_ragged_paged_scale",
     "kproj_exact", "kproj_rows", "quantize_runs",
     "token_slots", "attention_ragged_paged", "cache_rows", "tables_ragged_paged",
+    "attention_tree_ragged_paged", "kv_keep_ragged_paged", "kv_read_ragged_paged", "release_ragged_paged", "rope",
+    "rope_ragged_paged", "tree_mask",
 ]
