@@ -44,6 +44,7 @@ SOURCE_FLAGS = {
     "w4_decode.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=16"],
     "attention_rows.hip": ["-mllvm", "-enable-ipra=0"],
     "attention_rows_tree.hip": ["-mllvm", "-enable-ipra=0"],
+    "attention_tile_tree.hip": ["-mllvm", "-enable-ipra=0"],
 }
 
 

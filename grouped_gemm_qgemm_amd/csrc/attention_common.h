@@ -184,7 +184,7 @@ __device__ __forceinline__ int attn_chunks(int span, int chunk) { return span <=
 // Item `want` of each head; all NT threads call it. Items are ordered
 // by sequence, then chunk, then tile (the last tiles, which see the most positions,
 // first). Workgroup 0 also writes the workspace's count of records.
-template <int NT, bool TREE>
+template <int NT>
 __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, AttnScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   if (p.batch <= 64) {
@@ -196,7 +196,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
       fresh = (int)p.offs[lane + 1] - row0;
       len = fresh + (int)p.cache_len[lane];
     }
-    const int tiles = attn_tiles(p, fresh), span = attn_span<TREE>(p, len, fresh);
+    const int tiles = attn_tiles(p, fresh), span = attn_span<false>(p, len, fresh);
     unsigned long long all = lane < p.batch ? (unsigned long long)tiles * (unsigned)span : 0;
 #pragma unroll
     for (int d = 32; d >= 1; d >>= 1) all += __shfl_xor(all, d);
@@ -244,7 +244,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
       const int row0 = (int)p.offs[b], fresh = (int)p.offs[b + 1] - row0;
       const int len = fresh + (int)p.cache_len[b];
       if (b0 == 0) { row00 = row0; fresh0 = fresh; len0 = len; }
-      cost += (unsigned long long)attn_tiles(p, fresh) * (unsigned)attn_span<TREE>(p, len, fresh);
+      cost += (unsigned long long)attn_tiles(p, fresh) * (unsigned)attn_span<false>(p, len, fresh);
     }
   }
 #pragma unroll
@@ -268,7 +268,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
         len = fresh + (int)p.cache_len[b];
       }
       tiles = attn_tiles(p, fresh);
-      if (tiles) ns = attn_chunks(attn_span<TREE>(p, len, fresh), chunk);
+      if (tiles) ns = attn_chunks(attn_span<false>(p, len, fresh), chunk);
     }
     const int items = tiles * ns, cuts = ns > 1 ? tiles : 0, slots = cuts * ns * p.hkv;
     int ii = items, is = slots, ic = cuts;
@@ -387,7 +387,9 @@ struct ShareScan {
 
 // Workgroups go to the eight XCDs in turn: all heads of a piece to one of them, so that
 // its L2 gets whole cache rows (and scale lines), not every eighth 256 bytes.
-template <int NT, bool TREE>
+//
+// LEAST: units of a share, at least, with one head per workgroup.
+template <int NT, bool TREE, int LEAST>
 __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>& sh) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const bool one_wave = p.batch <= 64;   // every wave looks at all sequences, one per lane: no barrier
@@ -432,7 +434,7 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
   // against 15.0, 16 of 2000 36 against 34, 32 of 2000 51 against 54, 64 of 1 to 8192 214 against 204).
   const bool wide = (unsigned long long)s.cut.units * (p.hkv / p.hw) >= (unsigned long long)kWideBlocks * p.target;
   s.hw = wide ? p.hw : 1;
-  const int groups = wide ? p.hkv / p.hw : p.hkv, least = wide ? 1 : NT / 64;
+  const int groups = wide ? p.hkv / p.hw : p.hkv, least = wide ? 1 : LEAST;
   const uint32_t at8 = blockIdx.x / 8;
   s.h = at8 % groups * s.hw;
   s.w = at8 / groups * 8 + blockIdx.x % 8;
@@ -518,6 +520,55 @@ __device__ __forceinline__ AttnShare attn_share(const AttnArgs& p, ShareScan<NT>
   s.at = s.cut.start(w);
   s.end = s.cut.start(w + 1);
   return s;
+}
+
+// The part of a share that lies in the tile it stands at: `take` units, positions [first, end)
+// (none where the tile ends before its sequence's longest does), and the workspace's slot for
+// them, -1 where they are the whole tile.
+struct AttnPart {
+  int take, first, end, slot;
+};
+template <bool TREE>
+__device__ __forceinline__ AttnPart attn_part(const AttnArgs& p, const AttnShare& s, const AttnTile& t) {
+  const int un = attn_units<TREE>(p, s.fresh + s.cached, s.fresh);   // the tile's units: [first_unit, first_unit + un)
+  const uint32_t first_unit = s.at - s.in_tile;
+  AttnPart part;
+  part.take = min((int)(s.end - s.at), un - s.in_tile);
+  // (a tile's first unit may begin with positions, and pages, that nobody sees)
+  const int from = t.start + s.in_tile * p.step;
+  part.first = max(from, t.begin & ~31);
+  part.end = min(t.end, from + part.take * p.step);
+  part.slot = -1;
+  if (part.first >= part.end) return part;
+  const uint32_t last_unit = first_unit + ((t.end - t.start + p.step - 1) >> p.step_log2) - 1;
+  const uint32_t begin = s.cut.start(s.w);
+  // a share's first part goes to its slot 2 w, its last to 2 w + 1; those between are whole tiles
+  if (first_unit < begin || last_unit >= s.end) part.slot = (2 * s.w + (s.at == begin ? 0 : 1)) * p.hkv + s.h;
+  if (first_unit < begin && s.h == 0 && threadIdx.x == 0) {
+    const int w0 = s.cut.of(first_unit);
+    if (s.w == w0 + 1) {                                       // the tile's second share describes it for the join
+      const int first = 2 * w0 + (first_unit == s.cut.start(w0) ? 0 : 1);
+      *attn_record(p, s.w) = AttnRecord{(int)s.cut.of(last_unit) - w0 + 1, s.row0, t.r_first, t.r_count, first * p.hkv,
+                                        2 * s.w * p.hkv, 2 * p.hkv, 1};
+    }
+  }
+  return part;
+}
+// On to the share's next tile, after `take` units of this one; false at its end.
+__device__ __forceinline__ bool attn_next(const AttnArgs& p, AttnShare& s, int take) {
+  s.at += take;
+  if (s.at >= s.end) return false;
+  s.in_tile = 0;
+  if (++s.tile == attn_tiles(p, s.fresh)) {            // on to the next sequence that has tiles
+    s.tile = 0;
+    do {
+      ++s.b;
+      s.row0 = (int)p.offs[s.b];
+      s.fresh = (int)p.offs[s.b + 1] - s.row0;
+    } while (s.fresh == 0);
+    s.cached = (int)p.cache_len[s.b];
+  }
+  return true;
 }
 
 // four e4m3 codes -> four bf16 (exact)
@@ -629,6 +680,9 @@ void attention_rows_shape(AttnArgs& p, int mt);
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_rows_tree(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
-hipError_t launch_attention_tiles_tree(const AttnArgs& p, unsigned grid, hipStream_t stream);
+// The same for trees with many rows: rows per tile, and workgroups that run at once. tall: tiles
+// of 256 rows where there are such instances, else of 128.
+void attention_tree_shape(AttnArgs& p, bool tall);
+hipError_t launch_attention_tree(const AttnArgs& p, bool tall, unsigned grid, hipStream_t stream);
 
 }  // namespace qg

@@ -30,6 +30,7 @@ constexpr int kRowsMost = 512, kRowsStep = 32, kRowsHeads = 4;
 // of all tiles' positions, so batches of several prompts are not: of those eight, played
 // through in launch order, the last workgroup ends after 16 blocks where the mean is 11.
 constexpr int kTileTarget = 512, kTileMinChunk = 256, kTileStep = 64;
+constexpr int kTreeRows = kTileTarget * 128;   // of all of a tree call's workgroups that run at once, at most
 
 constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
@@ -193,6 +194,19 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const long long pieces = std::max(wide, narrow);
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
   }
+  if (p.tree) {
+    const bool tall = rows > 128LL * p.batch;
+    attention_tree_shape(p, tall);
+    p.target = std::max<int>(std::min<int>(p.target, kTreeRows / p.bm), p.hkv);
+    set_shape(p, p.bm, kTileStep);
+    const long long tree_tiles = rows / p.bm + p.batch;
+    while ((room + p.step - 1) / p.step > INT32_MAX / tree_tiles) set_shape(p, p.bm, 2 * p.step);   // units are counted in 32 bits
+    const long long pieces = std::min<long long>(p.target / p.hkv, tree_tiles * ((room + p.step - 1) / p.step));
+    const long long grid = (pieces + 7) / 8 * 8 * p.hkv;
+    if (grid > kMostWorkgroups) return hipErrorNotSupported;
+    const hipError_t e = launch_attention_tree(p, tall, (unsigned)grid, stream);
+    return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);
+  }
   p.min_chunk = kTileMinChunk;
   p.target = tile_target(p.hkv);
   p.target_log2 = log2_of(p.target);
@@ -202,7 +216,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   const long long chunks = (room + p.min_chunk - 1) / p.min_chunk;
   const long long items = std::min(tiles + p.target / p.hkv + 1, chunks < tiles + p.target ? tiles * chunks : (long long)INT64_MAX);
   if (items > kMostWorkgroups / p.hkv) return hipErrorNotSupported;
-  const hipError_t e = (p.tree ? launch_attention_tiles_tree : launch_attention_tiles)(p, (unsigned)(items * p.hkv), stream);
+  const hipError_t e = launch_attention_tiles(p, (unsigned)(items * p.hkv), stream);
   // tiles that are cut have at least two slots each, of fewer than 2 target
   return e != hipSuccess || chunks <= 1 ? e : launch_join(p, std::min(tiles, (long long)(p.target / p.hkv + 1)), stream);
 }

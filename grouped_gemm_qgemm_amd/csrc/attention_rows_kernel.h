@@ -544,7 +544,7 @@ constexpr int attn_waves(int nw) { return attn_resident<Lds>(nw) * nw >= 8 ? 2 :
 template <int DP, int GRAN, int MT, int NW, int NST, bool TREE>
 __global__ __launch_bounds__(NW * 64, (attn_waves<AttnRowsLds<DP, GRAN, MT, NW, NST>>(NW))) void attention_rows_kernel(AttnArgs p) {
   __shared__ AttnRowsLds<DP, GRAN, MT, NW, NST> lds;
-  AttnShare s = attn_share<NW * 64, TREE>(p, lds.scan);
+  AttnShare s = attn_share<NW * 64, TREE, NW>(p, lds.scan);
   if (s.b < 0) return;
   while (true) {
     AttnItem it{};
@@ -554,40 +554,14 @@ __global__ __launch_bounds__(NW * 64, (attn_waves<AttnRowsLds<DP, GRAN, MT, NW, 
     it.fresh = s.fresh;
     it.cached = s.cached;
     const AttnTile t = attn_tile<TREE>(p, it);
-    const int un = attn_units<TREE>(p, s.fresh + s.cached, s.fresh);          // the tile's units: [first_unit, first_unit + un)
-    const uint32_t first_unit = s.at - s.in_tile;
-    const int take = min((int)(s.end - s.at), un - s.in_tile);
-    // (a tile's first unit may begin with positions, and pages, that nobody sees)
-    const int from = t.start + s.in_tile * p.step, c_first = max(from, t.begin & ~31), c_end = min(t.end, from + take * p.step);
-    if (c_first < c_end) {                                     // a tile may end before its sequence's longest does
-      const uint32_t last_unit = first_unit + ((t.end - t.start + p.step - 1) >> p.step_log2) - 1;
-      const uint32_t begin = s.cut.start(s.w);
-      // a share's first part goes to its slot 2 w, its last to 2 w + 1; those between are whole tiles
-      const int slot = first_unit >= begin && last_unit < s.end ? -1 : (2 * s.w + (s.at == begin ? 0 : 1)) * p.hkv + s.h;
-      if (first_unit < begin && s.h == 0 && threadIdx.x == 0) {
-        const int w0 = s.cut.of(first_unit);
-        if (s.w == w0 + 1) {                                     // the tile's second share describes it for the join
-          const int first = 2 * w0 + (first_unit == s.cut.start(w0) ? 0 : 1);
-          *attn_record(p, s.w) = AttnRecord{(int)s.cut.of(last_unit) - w0 + 1, it.row0, t.r_first, t.r_count, first * p.hkv,
-                                            2 * s.w * p.hkv, 2 * p.hkv, 1};
-        }
-      }
+    const AttnPart part = attn_part<TREE>(p, s, t);
+    if (part.first < part.end) {
       AttnRepeat none[MT];
-      if (attend_rows<DP, GRAN, MT, NW, NST, false, TREE>(p, it, s.h, s.hw, c_first, c_end, slot, lds, none))
-        attend_rows_safe<DP, GRAN, MT, NW, NST, TREE>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, s.hw, c_first, c_end, slot, &lds);
+      if (attend_rows<DP, GRAN, MT, NW, NST, false, TREE>(p, it, s.h, s.hw, part.first, part.end, part.slot, lds, none))
+        attend_rows_safe<DP, GRAN, MT, NW, NST, TREE>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, s.hw, part.first,
+                                                      part.end, part.slot, &lds);
     }
-    s.at += take;
-    if (s.at >= s.end) return;
-    s.in_tile = 0;
-    if (++s.tile == attn_tiles(p, s.fresh)) {            // on to the next sequence that has tiles
-      s.tile = 0;
-      do {
-        ++s.b;
-        s.row0 = (int)p.offs[s.b];
-        s.fresh = (int)p.offs[s.b + 1] - s.row0;
-      } while (s.fresh == 0);
-      s.cached = (int)p.cache_len[s.b];
-    }
+    if (!attn_next(p, s, part.take)) return;
     __syncthreads();   // the next part's loads overwrite what the last one's join read
   }
 }

@@ -51,7 +51,6 @@ namespace qg {
 
 namespace {
 
-constexpr int AW = 4;                // waves
 constexpr int TPG = 1024;            // page table entries held in LDS at a time
 
 // 16-byte chunk c of LDS row r (DP bf16 elements) lies at c ^ swz(r): the 16 rows of a
@@ -64,10 +63,9 @@ __device__ __forceinline__ int swz_t(int r) {
 
 }  // namespace
 
-// LDS of a workgroup.
-template <int DP, int GRAN>
+// LDS of a workgroup of AW waves. KB: positions per block.
+template <int DP, int GRAN, int AW, int KB>
 struct AttnTileLds {
-  static constexpr int KB = DP > 128 ? 32 : 64;             // positions per block
   static constexpr int R = GRAN > 0 ? DP / GRAN : 1;        // scale runs per head, at most
   __attribute__((aligned(16))) u32x4_t ring[2][2][KB * DP / 8];                                   // [block parity][keys, values]
   __attribute__((aligned(16))) float ring_s[GRAN > 0 ? 2 : 1][2][R][GRAN > 0 ? KB : 1];   // [keys, values][run][position]
@@ -76,42 +74,71 @@ struct AttnTileLds {
   AttnScan<AW * 64> scan;
 };
 
-// One item. GRAN: head-dim elements per scale of an e4m3 cache, 0 for bf16. SAFE:
-// values are selected per token. Returns whether some row has to be computed again
-// (without SAFE: sums are too large, infinities, NaN or zero; with it: as `rep`, the
+// A wave's rows: the result, or (slot >= 0) the part of it with its reference and sum.
+template <int DP, bool TREE>
+__device__ __forceinline__ void store_tile(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int slot,
+                                           const float16_t (&acc)[DP / 32], float m, float sum) {
+  constexpr int ND = DP / 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(p.bm, DP);
+  const int r = wave * 32 + col;
+  if (r >= t.r_count) return;
+  if (slot < 0) {
+    const float inv = TREE && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
+    const int row = t.r_first + r, token = over_group(p, row);
+    uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int d = n * 32 + 8 * g + 4 * half;
+        if (d < p.d)
+          *reinterpret_cast<u32x2_t*>(to + d) = u32x2_t{f2bf2_rn(acc[n][4 * g] * inv, acc[n][4 * g + 1] * inv),
+                                                        f2bf2_rn(acc[n][4 * g + 2] * inv, acc[n][4 * g + 3] * inv)};
+      }
+  } else {
+#pragma unroll
+    for (int n = 0; n < ND; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + n * 32 + 8 * g + 4 * half) =
+            float4_t{acc[n][4 * g], acc[n][4 * g + 1], acc[n][4 * g + 2], acc[n][4 * g + 3]};
+    if (half == 0) {
+      ws[(size_t)p.bm * DP + 2 * r] = m;
+      ws[(size_t)p.bm * DP + 2 * r + 1] = sum;
+    }
+  }
+}
+
+// Positions [c_first, c_end) of one tile, which are all of them where `slot` is -1 and go to
+// that slot of the workspace else. GRAN: head-dim elements per scale of an e4m3 cache, 0
+// for bf16. SAFE: values are selected per token. Returns whether some row has to be computed
+// again (without SAFE: sums are too large, infinities, NaN or zero; with it: as `rep`, the
 // state of this lane's row, says), for the whole workgroup, and then has written nothing.
-template <int DP, int GRAN, bool SAFE, bool TREE>
-__device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, int h, AttnTileLds<DP, GRAN>& lds, AttnRepeat& rep) {
+template <int DP, int GRAN, int AW, int KB, bool SAFE, bool TREE>
+__device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int c_first, int c_end,
+                                            int slot, AttnTileLds<DP, GRAN, AW, KB>& lds, AttnRepeat& rep) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int NT = AW * 64;
-  constexpr int KB = AttnTileLds<DP, GRAN>::KB;
   constexpr int NB = KB / 32;
   constexpr int NS = DP / 16;                 // MFMA steps of a score
   constexpr int ND = DP / 32;                 // 32-wide strips of the output
   constexpr int CH = DP / 8;                  // 16-byte chunks per LDS row
   constexpr int TILE = KB * CH;
   constexpr int LD = TILE / NT;               // direct loads per lane for the keys (or values) of a block
-  constexpr int R = AttnTileLds<DP, GRAN>::R;
+  constexpr int R = AttnTileLds<DP, GRAN, AW, KB>::R;
   constexpr int RS = FP8 ? GRAN / 16 : NS;    // MFMA steps per run
   constexpr int LC = FP8 ? DP / 16 : 1;       // e4m3: 16-code loads per row
   constexpr int LQ = FP8 ? KB * LC / NT : 0;  // e4m3: loads per thread for the keys (or values)
   constexpr int LS = FP8 ? (2 * KB * R + NT - 1) / NT : 0;   // scales per thread
+  static_assert(LD >= 1 && (!FP8 || LQ >= 1), "a block is at least one load of every thread");
   auto& ring = lds.ring;
   auto& ring_s = lds.ring_s;
   auto& pages = lds.pages;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, half = lane >> 5;
-  const AttnTile t = attn_tile<TREE>(p, it);
-  const int c_first = t.start + it.split * it.chunk;          // this item's positions [c_first, c_end)
-  const int c_end = min(t.end, c_first + it.chunk);
-  if (c_first >= c_end) return false;                               // the sequence's longer tiles need this chunk
-  const bool alone = t.end - t.start <= it.chunk;
-  if (!SAFE && it.nsplit > 1 && it.split == 0 && h == 0 && threadIdx.x == 0) {   // one workgroup describes the tile for the join
-    const int first = (it.slots + it.tile * p.hkv * it.nsplit);
-    *attn_record(p, it.record) = AttnRecord{(t.end - t.start + it.chunk - 1) / it.chunk, it.row0, t.r_first, t.r_count,
-                                            first, first + 1, 1, it.nsplit};
-  }
 
   const int rows = it.fresh * p.group;
   const int my_row = min(t.r_first + wave * 32 + col, rows - 1), tok = over_group(p, my_row);
@@ -161,7 +188,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[n][i] = 0.f;
     // as many positions at a time as the list of pages covers
-    const int seg = by16 ? it.chunk : (int)min((long long)it.chunk, (long long)(TPG - 1) * p.page_size / KB * KB);
+    const int seg = by16 ? c_end - c_first : (int)min((long long)(c_end - c_first), (long long)(TPG - 1) * p.page_size / KB * KB);
     for (int s_first = c_first; s_first < c_end; s_first += seg) {
       const int s_end = min(c_end, s_first + seg);
       const int page0 = by16 ? 0 : fast_div(max(s_first, t.begin), p.div_mul, p.div_shift);
@@ -512,79 +539,45 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
   }
 
-  const int slot = it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
-  float* ws = p.workspace + attn_header_floats(p.target) + (size_t)slot * attn_slot_floats(p.bm, DP);
-  const int r = wave * 32 + col;
-  if (r >= t.r_count) return false;
-  if (alone) {
-    const float inv = TREE && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
-    const int row = t.r_first + r, token = over_group(p, row);
-    uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
-#pragma unroll
-    for (int n = 0; n < ND; ++n)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int d = n * 32 + 8 * g + 4 * half;
-        if (d < p.d)
-          *reinterpret_cast<u32x2_t*>(to + d) = u32x2_t{f2bf2_rn(acc[n][4 * g] * inv, acc[n][4 * g + 1] * inv),
-                                                        f2bf2_rn(acc[n][4 * g + 2] * inv, acc[n][4 * g + 3] * inv)};
-      }
-  } else {
-#pragma unroll
-    for (int n = 0; n < ND; ++n)
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + n * 32 + 8 * g + 4 * half) =
-            float4_t{acc[n][4 * g], acc[n][4 * g + 1], acc[n][4 * g + 2], acc[n][4 * g + 3]};
-    if (half == 0) {
-      ws[(size_t)p.bm * DP + 2 * r] = SAFE ? rep.reference(m) : m;
-      ws[(size_t)p.bm * DP + 2 * r + 1] = sum;
-    }
-  }
+  store_tile<DP, TREE>(p, it, t, h, slot, acc, SAFE ? rep.reference(m) : m, sum);
   return false;
 }
 
 // Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
-template <int DP, int GRAN, bool TREE>
-__device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, AttnTileLds<DP, GRAN>* lds) {
+template <int DP, int GRAN, int AW, int KB, bool TREE>
+__device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, int h, int c_first, int c_end, int slot,
+                                                           AttnTileLds<DP, GRAN, AW, KB>* lds) {
   const AttnArgs p = reload_args(args);
+  const AttnItem item = uniform(it);
+  const AttnTile t = attn_tile<TREE>(p, item);
   AttnRepeat rep;
   for (int pass = 0; pass < kRepeats; ++pass)
-    if (!attend_tile<DP, GRAN, true, TREE>(p, uniform(it), blockIdx.x % p.hkv, *lds, rep)) return;
+    if (!attend_tile<DP, GRAN, AW, KB, true, TREE>(p, item, t, __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(c_first),
+                                               __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds, rep))
+      return;
 }
 
-template <int DP, int GRAN, bool TREE>
-__global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
-  __shared__ AttnTileLds<DP, GRAN> lds;
+// A workgroup per item (see attn_locate): of a causal call, tiles and parts differ in length.
+template <int DP, int GRAN>
+__global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void attention_tile_kernel(AttnArgs p) {
+  constexpr int AW = 4, KB = DP > 128 ? 32 : 64;
+  __shared__ AttnTileLds<DP, GRAN, AW, KB> lds;
   const int h = blockIdx.x % p.hkv;
-  const AttnItem it = attn_locate<AW * 64, TREE>(p, blockIdx.x / p.hkv, lds.scan);
+  const AttnItem it = attn_locate<AW * 64>(p, blockIdx.x / p.hkv, lds.scan);
   if (it.b < 0) return;
-  AttnRepeat none;
-  if (attend_tile<DP, GRAN, false, TREE>(p, it, h, lds, none))
-    attend_tile_safe<DP, GRAN, TREE>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, &lds);
-}
-
-template <bool TREE>
-static hipError_t launch_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream) {
-#define QG_ATTN(DP, GRAN) attention_tile_kernel<DP, GRAN, TREE><<<grid, AW * 64, 0, stream>>>(p)
-  const int gran = p.fp8 ? p.gran : 0;
-  if (p.d <= 64) {
-    if (gran == 0) QG_ATTN(64, 0);
-    else if (gran == 32) QG_ATTN(64, 32);
-    else QG_ATTN(64, 64);
-  } else if (p.d <= 128) {
-    if (gran == 0) QG_ATTN(128, 0);
-    else if (gran == 32) QG_ATTN(128, 32);
-    else if (gran == 64) QG_ATTN(128, 64);
-    else QG_ATTN(128, 128);
-  } else {
-    if (gran == 0) QG_ATTN(256, 0);
-    else if (gran == 32) QG_ATTN(256, 32);
-    else if (gran == 64) QG_ATTN(256, 64);
-    else QG_ATTN(256, 128);
+  const AttnTile t = attn_tile<false>(p, it);
+  const int c_first = t.start + it.split * it.chunk;          // this item's positions [c_first, c_end)
+  const int c_end = min(t.end, c_first + it.chunk);
+  if (c_first >= c_end) return;                               // the sequence's longer tiles need this chunk
+  if (it.nsplit > 1 && it.split == 0 && h == 0 && threadIdx.x == 0) {   // one workgroup describes the tile for the join
+    const int first = (it.slots + it.tile * p.hkv * it.nsplit);
+    *attn_record(p, it.record) = AttnRecord{(t.end - t.start + it.chunk - 1) / it.chunk, it.row0, t.r_first, t.r_count,
+                                            first, first + 1, 1, it.nsplit};
   }
-#undef QG_ATTN
-  return hipGetLastError();
+  const int slot = t.end - t.start <= it.chunk ? -1 : it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
+  AttnRepeat none;
+  if (attend_tile<DP, GRAN, AW, KB, false, false>(p, it, t, h, c_first, c_end, slot, lds, none))
+    attend_tile_safe<DP, GRAN, AW, KB, false>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, h, c_first, c_end, slot, &lds);
 }
 
 }  // namespace qg

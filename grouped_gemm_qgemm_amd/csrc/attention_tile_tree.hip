@@ -1,10 +1,56 @@
 // The kernel for many rows: instances for attention_tree_ragged_paged.
-#include "attention_tile_kernel.h"
+#include "attention_tree_kernel.h"
 
 namespace qg {
 
-hipError_t launch_attention_tiles_tree(const AttnArgs& p, unsigned grid, hipStream_t stream) {
-  return launch_tiles<true>(p, grid, stream);
+namespace {
+
+// f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call.
+template <typename F>
+void with_tree_kernel(const AttnArgs& p, bool tall, F&& f) {
+#define QG_ATTN(DP, GRAN)                                                                                          \
+  do {                                                                                                             \
+    if (odd) f(attention_tree_kernel<DP, GRAN, 4, true>, 4, AttnTreeLds<DP, GRAN, 4, true>::ONE ? 1 : 2);            \
+    else f(attention_tree_kernel<DP, GRAN, 4, false>, 4, AttnTreeLds<DP, GRAN, 4, false>::ONE ? 1 : 2);              \
+  } while (0)
+#define QG_ATTN_TALL(GRAN)                                                     \
+  do {                                                                         \
+    if (tall && !odd) f(attention_tree_kernel<128, GRAN, 8, false>, 8, 1);     \
+    else QG_ATTN(128, GRAN);                                                   \
+  } while (0)
+  const bool odd = p.page_size % 16 != 0;
+  const int gran = p.fp8 ? p.gran : 0;
+  if (p.d <= 64) {
+    if (gran == 0) QG_ATTN(64, 0);
+    else if (gran == 32) QG_ATTN(64, 32);
+    else QG_ATTN(64, 64);
+  } else if (p.d <= 128) {
+    if (gran == 0) QG_ATTN_TALL(0);
+    else if (gran == 32) QG_ATTN_TALL(32);
+    else if (gran == 64) QG_ATTN_TALL(64);
+    else QG_ATTN_TALL(128);
+  } else {
+    if (gran == 0) QG_ATTN(256, 0);
+    else if (gran == 32) QG_ATTN(256, 32);
+    else if (gran == 64) QG_ATTN(256, 64);
+    else QG_ATTN(256, 128);
+  }
+#undef QG_ATTN
+#undef QG_ATTN_TALL
+}
+
+}  // namespace
+
+void attention_tree_shape(AttnArgs& p, bool tall) {
+  with_tree_kernel(p, tall, [&](auto, int nw, int resident) {
+    p.bm = 32 * nw;
+    p.target = p.num_cus * resident;
+  });
+}
+
+hipError_t launch_attention_tree(const AttnArgs& p, bool tall, unsigned grid, hipStream_t stream) {
+  with_tree_kernel(p, tall, [&](auto kernel, int nw, int) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
+  return hipGetLastError();
 }
 
 }  // namespace qg
