@@ -174,8 +174,15 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   // 38 against 32). Beyond 32 rows it loses (32 sequences of 16 tokens on 4000: bf16 186 us
   // against 117, e4m3 134 against 114). A few long chunks among many single tokens go by the
   // average too: 256 tokens on 1000 and a chunk of 512 after 8000, bf16 863 us, 281 us as two calls.
+  //
+  // Trees have a kernel of their own for many rows, which on bf16 caches is the faster one from 17
+  // rows on (32 trees of 6 tokens on 4000: 123 us against 129, 64 of 8 on 1000 54 against 70, heads
+  // of 256 212 against 238), but not with 16 or fewer (32 of 4 on 4000: 121 against 112, heads of 256 212
+  // against 205; heads of 64 57 against 67), and on e4m3 where the other is (32 of 8 on 4000: 110 against
+  // 90; 8 of them 48 against 52; heads of 256, 8 of 8, 117 against 94).
   const int mt = rows > 16LL * p.batch ? 2 : 1;
-  const bool few = mt == 1 || (rows <= 32LL * p.batch && (4LL * p.batch * p.hkv > p.num_cus || (p.fp8 && p.d > 128)));
+  const bool some = (!p.tree || p.fp8) && rows <= 32LL * p.batch && (4LL * p.batch * p.hkv > p.num_cus || (p.fp8 && p.d > 128));
+  const bool few = mt == 1 || some;
   set_shape(p, few ? 16 * mt : 128, few ? kRowsStep : kTileStep);
   // sequence b has ceil(new_b * group / bm) tiles per key/value head, of at most `room` positions
   const long long tiles = rows / p.bm + p.batch, room = p.max_pages * p.page_size;
@@ -195,9 +202,11 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);   // one piece has all its tiles whole
   }
   if (p.tree) {
+    // Tiles of 256 rows where 128 are not enough for most sequences: 32 trees of 64 tokens, 4 heads to one,
+    // on up to 8191 positions 200 us against 247, 6 of 20 to 120 on up to 40000 (e4m3) 457 against 503.
     const bool tall = rows > 128LL * p.batch;
     attention_tree_shape(p, tall);
-    p.target = std::max<int>(std::min<int>(p.target, kTreeRows / p.bm), p.hkv);
+    p.target = std::max<int>(std::min<int>(p.target, kTreeRows / p.bm), p.hkv);   // the workspace's slots
     set_shape(p, p.bm, kTileStep);
     const long long tree_tiles = rows / p.bm + p.batch;
     while ((room + p.step - 1) / p.step > INT32_MAX / tree_tiles) set_shape(p, p.bm, 2 * p.step);   // units are counted in 32 bits

@@ -571,10 +571,16 @@ namespace {
 // f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call.
 template <bool TREE, typename F>
 void with_rows_kernel(const AttnArgs& p, int mt, F&& f) {
-#define QG_ATTN(DP, GRAN, NW, NST)                                                                                    \
-  do {                                                                                                                \
-    if (mt == 1) f(attention_rows_kernel<DP, GRAN, 1, NW, NST, TREE>, NW, attn_resident<AttnRowsLds<DP, GRAN, 1, NW, NST>>(NW)); \
-    else f(attention_rows_kernel<DP, GRAN, 2, NW, NST, TREE>, NW, attn_resident<AttnRowsLds<DP, GRAN, 2, NW, NST>>(NW));         \
+  // (trees on bf16 caches come here with up to 16 rows only)
+#define QG_ATTN(DP, GRAN, NW, NST)                                                                                               \
+  do {                                                                                                                           \
+    if constexpr (!TREE || GRAN > 0) {                                                                                           \
+      if (mt == 2) {                                                                                                             \
+        f(attention_rows_kernel<DP, GRAN, 2, NW, NST, TREE>, NW, attn_resident<AttnRowsLds<DP, GRAN, 2, NW, NST>>(NW));          \
+        break;                                                                                                                   \
+      }                                                                                                                          \
+    }                                                                                                                            \
+    f(attention_rows_kernel<DP, GRAN, 1, NW, NST, TREE>, NW, attn_resident<AttnRowsLds<DP, GRAN, 1, NW, NST>>(NW));              \
   } while (0)
   const int gran = p.fp8 ? p.gran : 0;
   if (p.d <= 64) {

@@ -63,7 +63,7 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
   constexpr int RS = FP8 ? GRAN / 16 : NS;    // MFMA steps per run
   // Fragments read ahead of their MFMAs. Left to itself the compiler reads each right before its
   // MFMA and waits out the LDS latency every time.
-  constexpr int PF = FP8 ? 4 : 4;
+  constexpr int PF = 4;
   static_assert(PW == 8 || PW == 16, "a wave's positions lie in one page");
   static_assert(LD >= 1 && LB * (FP8 ? NRAW : NST) < 64, "loads in flight that a wait can count");
   auto& ring = lds.b.ring;
@@ -82,8 +82,6 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
     const int d = 16 * s + 8 * half;
     qf[s] = d < p.d ? *reinterpret_cast<const u32x4_t*>(q + d) : u32x4_t{0, 0, 0, 0};
   }
-#pragma unroll
-  for (int s = 0; s < NS; ++s) arrived(qf[s]);
   const float cs = p.scale * kLog2e;
   const int runs = FP8 ? p.d / (FP8 ? GRAN : 1) : 1;
   if (p.d < DP) {                             // chunks of an LDS row that do not exist are zero from here on
@@ -260,8 +258,11 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
     // S^T = K Q^T of the block at x
     auto score = [&](Scores& sc, const Place& x) {
       constexpr int KS = NB * NS, G = KS / RS;     // MFMAs, runs of them (of one nb each)
+      // bf16: the halves of a block in turn, as an MFMA waits for the sum that it adds to
+      auto step_of = [&](int j) { return FP8 ? j % NS : j / NB; };
+      auto half_of = [&](int j) { return FP8 ? j / NS : j % NB; };
       auto frag = [&](int j) {
-        return *reinterpret_cast<const u32x4_t*>(blocks_at + ((x.base + k_at) ^ (32 * (j % NS))) + j / NS * 32 * ROW);
+        return *reinterpret_cast<const u32x4_t*>(blocks_at + ((x.base + k_at) ^ (32 * step_of(j))) + half_of(j) * 32 * ROW);
       };
       __builtin_amdgcn_s_setprio(1);
       u32x4_t f[PF];
@@ -284,16 +285,16 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
-        const int g = j / RS;
+        const int g = FP8 ? j / RS : half_of(j);
         float16_t& to = sums(g);
-        if (j % RS == 0) {
+        if (step_of(j) % RS == 0) {
           if constexpr (FP8) {
             if (g > 0) scales(g - 1);
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) to[e] = 0.f;
         }
-        to = mfma32x32x16_bf16(f[j % PF], qf[j % NS], to);
+        to = mfma32x32x16_bf16(f[j % PF], qf[step_of(j)], to);
         if (j + PF < KS) f[j % PF] = frag(j + PF);
         if (FP8 && j % RS == RS - 1 && g > 0) scaled(g - 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -384,6 +385,8 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
       for (int u = 0; u < NST - 1; ++u)
         if (u < blocks) issue(u, u);
     }
+#pragma unroll
+    for (int n = 0; n < NS; ++n) arrived(qf[n]);   // (with the first blocks, which are waited for next anyway)
     int at = 0;
     for (int i = 0; i < blocks; ++i, at = at + 1 == NST ? 0 : at + 1) {
       if constexpr (!FP8) wait_blocks<LB, NST - 2>(blocks - 1 - i);

@@ -292,8 +292,10 @@ hipError_t launch_tables_ragged(const TablesArgs& p, hipStream_t stream) {
 hipError_t launch_release_ragged(const ReleaseArgs& p, hipStream_t stream) {
   uint32_t mul, shift;
   divide_by_page(p.page_size, mul, shift);
-  // a workgroup per 256 sequences, whose pages only the device knows
-  const int grid = (p.batch + TT - 1) / TT;
+  // How many pages go back only the device knows: no more than the stack has room for. A page per
+  // thread (4096 sequences, 35000 pages: 16 workgroups 15.0 us, then 9 pages per thread).
+  const long long want = (p.free_len + TT - 1) / TT;
+  const int grid = (int)(want < 1 ? 1 : want > 2 * p.num_cus ? 2 * p.num_cus : want);
   release_ragged_kernel<<<grid, TT, 0, stream>>>(p.free_pages, p.result, p.table, p.held, p.kept, p.free_count, p.batch,
                                                  p.max_pages, (uint32_t)p.free_len, (uint32_t)p.page_size, mul, shift);
   return hipGetLastError();

@@ -6,12 +6,19 @@ import torch
 
 import oracle
 import synth
-from attention_shapes import kernel
+import attention_shapes
 from gpu_util import Guarded, bf16v, dev16, dev32, host16, say
 from test_gpu_attention import compare, place, workspace
 from test_gpu_attention_extremes import cus, huge_values, put
 
 pytestmark = pytest.mark.gpu
+
+
+def kernel(d, cus):
+    """The kernel that a call takes, as attention_shapes.kernel says it of the other calls: trees on
+    bf16 caches take the one for many rows from 17 rows per sequence and head on."""
+    form = attention_shapes.kernel(d, cus)
+    return "tile" if form == "rows2" and not d.gran else form
 
 
 def tree_rows(d, words, seed=0, kind="tree"):
@@ -174,7 +181,7 @@ FORMS = {
 def form_case(seed, form, dim, gran):
     new, hist, hq, hkv = FORMS[form]
     d = synth.attention_inputs(seed, new, hist, hq=hq, hkv=hkv, d=dim, gran=gran)
-    assert kernel(d, cus()) == form.split()[0]
+    assert attention_shapes.kernel(d, cus()) == form.split()[0]
     say(f"[tree] {form} head {dim} gran {gran}")
     return d
 
