@@ -486,7 +486,7 @@ static qg_status cache_args(const qg_paged_kv* kv, int64_t B, bool lengths, qg::
   out->fp8 = fp8 ? 1 : 0;
   return QG_OK;
 }
-constexpr int64_t kMostRows = 1 << 25;   // tokens or rows of a call: a launch has less than 2^32 threads
+constexpr int64_t kMostRows = 1 << 24;   // tokens, rows or sequences of a call: a launch has less than 2^32 threads
 
 // One of rope_ragged_paged's inputs [T, H, D], whose rows are `stride` elements apart.
 static qg_status check_rows(const qg_tensor* t, int64_t T, int64_t H, int64_t D, int64_t stride) {

@@ -467,8 +467,8 @@ qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* res
  *   positions  i32 [T] or NULL
  *   amplitude  finite (QG_ERR_INVALID_ARG otherwise)
  *
- * D is a multiple of 8 (QG_ERR_ALIGN), at most 1024 (QG_ERR_UNSUPPORTED). One of q and k
- * at least is given (QG_ERR_NULL). Offsets, lengths and page ids are not re-validated on
+ * D is a multiple of 8 (QG_ERR_ALIGN), at most 1024, and T at most 2^24 (QG_ERR_UNSUPPORTED). One
+ * of q and k at least is given (QG_ERR_NULL). Offsets, lengths and page ids are not re-validated on
  * the device; two tokens must not address one slot. q_out must not overlap q.
  */
 qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg_tensor* k, const qg_tensor* v,
@@ -490,8 +490,8 @@ qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg
  *   kv                  read only; cache_lengths is not used and may be NULL
  *   layer_idx           < L (QG_ERR_INVALID_ARG otherwise)
  *
- * D is a multiple of 8 (QG_ERR_ALIGN). Positions and page ids are not re-validated on the
- * device; only pages that hold a position of a range are read.
+ * D is a multiple of 8 (QG_ERR_ALIGN), T at most 2^24 (QG_ERR_UNSUPPORTED). Positions and page ids are
+ * not re-validated on the device; only pages that hold a position of a range are read.
  */
 qg_status kv_read_ragged_paged(const qg_tensor* k_out, const qg_tensor* v_out, const qg_tensor* output_row_offsets,
                                const qg_tensor* first_positions, const qg_paged_kv* kv, uint32_t layer_idx,
@@ -512,7 +512,8 @@ qg_status kv_read_ragged_paged(const qg_tensor* k_out, const qg_tensor* v_out, c
  *   kept    u32 [B]      at most M (more count as M)
  *   kv      the cache, updated in place; cache_lengths is not changed
  *
- * D is a multiple of 8 (QG_ERR_ALIGN). Positions and page ids are not re-validated on the device.
+ * D is a multiple of 8 (QG_ERR_ALIGN), B at most 2^22 (QG_ERR_UNSUPPORTED). Positions and page ids are not
+ * re-validated on the device.
  */
 qg_status kv_keep_ragged_paged(const qg_tensor* path, const qg_tensor* kept, const qg_paged_kv* kv,
                                hipStream_t stream);

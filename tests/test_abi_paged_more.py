@@ -275,3 +275,19 @@ def test_binding_refuses_what_a_descriptor_cannot_say():
         q._cache_record(blocks, t[:2], t[:1].view(1, 1), None, 0, 1)
     with pytest.raises(ValueError):
         q._cache_record(blocks, t[:1].long(), t[:1].view(1, 1), None, 0, 1)
+
+
+def test_more_rows_than_a_launch_has(lib):
+    bb = Buf()
+
+    def rows(n, shape, dtype):
+        t = bb.t(shape, dtype)
+        t.shape[0] = n   # the size is checked, the memory is not touched
+        return t
+
+    n = 2**24 + 1
+    assert rope(lib, bb, q_out=rows(n, (1, 4, 64), QG.BF16), q=rows(n, (1, 4, 64), QG.BF16), k=rows(n, (1, 2, 64), QG.BF16),
+                v=rows(n, (1, 2, 64), QG.BF16), pos=rows(n, (1,), QG.I32)) == QG.ERR_UNSUPPORTED
+    assert read(lib, bb, k=rows(n, (1, 2, 64), QG.BF16), v=rows(n, (1, 2, 64), QG.BF16)) == QG.ERR_UNSUPPORTED
+    n = 2**22 + 1
+    assert keep(lib, bb, path=rows(n, (1, 4), QG.I32), kept=rows(n, (1,), QG.U32)) == QG.ERR_UNSUPPORTED
