@@ -11,6 +11,11 @@
 // and reads the partner chunk as well where pairs are R / 2 apart: from the cache line that
 // another lane of its wave asked for anyway.
 //
+// 33000 tokens of 48 heads into e4m3 take 160 us, 5.2 TB/s read + written (a large copy:
+// 5.1 to 5.4), eight prompts (4300 tokens, bf16) 17.7 us, 64 tokens 5.4 us on the GPU. A thread
+// with the loads of one head in flight takes 167 us for the first of these, of two 173, of
+// four 163; four tokens per workgroup take 162 us.
+//
 // The angle a = position * f is a product of 31 and 24 bits, of which a far position keeps
 // few behind the point: its reduction carries what each 64-bit product rounds away, so that
 // every position's part of a turn is exact to fp32. From there on fp32 is enough.
@@ -21,7 +26,8 @@ namespace qg {
 namespace {
 
 constexpr int RT = 256;            // threads
-constexpr int RTOK = RT / 64;      // tokens per workgroup, at most
+constexpr int RTOK = 2;            // tokens per workgroup, at most (a wave each to find its place)
+constexpr int RHEADS = 3;          // heads whose loads a thread has in flight
 constexpr int RHALF = 512;         // angles per token, at most
 enum { PAIRS_APART = 0, PAIRS_ODD = 1, PAIRS_SIDE = 2 };   // R / 2 apart (a multiple of 8, or not), side by side
 
@@ -111,54 +117,68 @@ __global__ __launch_bounds__(RT) void rope_paged_kernel(RopeArgs p, int tokens) 
         if (!second) sn[i] = -sn[i];
       }
     }
-    for (int h = slot; h < heads; h += per) {
-      const bool is_q = h < hq, is_v = h >= hq + hkv;
-      const uint16_t* src = is_q ? p.q + r * p.q_stride + (size_t)h * d
-                            : is_v ? p.v + r * p.v_stride + (size_t)(h - hq - hkv) * d
-                                   : p.k + r * p.k_stride + (size_t)(h - hq) * d;
-      const u32x4_t raw = *reinterpret_cast<const u32x4_t*>(src + first);
-      float x[8];
-      unpack8(raw, x);
-      if (turned && !is_v) {
-        float y[8];                                // the other element of each pair
-        if (PAIRS == PAIRS_SIDE) {
+    for (int h0 = slot; h0 < heads; h0 += RHEADS * per) {
+      // the loads of several heads before the first of them is stored
+      u32x4_t raw[RHEADS], other[RHEADS];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
-        } else if (PAIRS == PAIRS_APART) {
-          unpack8(*reinterpret_cast<const u32x4_t*>(src + (first < half ? first + half : first - half)), y);
-        } else {
+      for (int u = 0; u < RHEADS; ++u) {
+        const int h = min(h0 + u * per, heads - 1);
+        const uint16_t* src = h < hq ? p.q + r * p.q_stride + (size_t)h * d
+                              : h >= hq + hkv ? p.v + r * p.v_stride + (size_t)(h - hq - hkv) * d
+                                              : p.k + r * p.k_stride + (size_t)(h - hq) * d;
+        raw[u] = *reinterpret_cast<const u32x4_t*>(src + first);
+        if (PAIRS == PAIRS_APART && turned && h < hq + hkv)
+          other[u] = *reinterpret_cast<const u32x4_t*>(src + (first < half ? first + half : first - half));
+      }
+#pragma unroll
+      for (int u = 0; u < RHEADS; ++u) {
+        const int h = h0 + u * per;
+        if (h >= heads) break;
+        const bool is_q = h < hq, is_v = h >= hq + hkv;
+        float x[8];
+        unpack8(raw[u], x);
+        if (turned && !is_v) {
+          float y[8];                                // the other element of each pair
+          if (PAIRS == PAIRS_SIDE) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+          } else if (PAIRS == PAIRS_APART) {
+            unpack8(other[u], y);
+          } else {
+            const uint16_t* src = is_q ? p.q + r * p.q_stride + (size_t)h * d : p.k + r * p.k_stride + (size_t)(h - hq) * d;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int e = first + i;
+              y[i] = bf2f(src[e >= 2 * half ? e : e < half ? e + half : e - half]);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int e = first + i;
-            y[i] = bf2f(src[e >= 2 * half ? e : e < half ? e + half : e - half]);
+            const bool in = PAIRS == PAIRS_APART || first + i < 2 * half;
+            x[i] = in ? __builtin_fmaf(x[i], cs[i], y[i] * sn[i]) : x[i];
           }
         }
+        if (is_q || !FP8) {
+          const u32x4_t o = {f2bf2_rn(x[0], x[1]), f2bf2_rn(x[2], x[3]), f2bf2_rn(x[4], x[5]), f2bf2_rn(x[6], x[7])};
+          uint16_t* to = is_q ? p.q_out + ((size_t)r * hq + h) * d
+                              : static_cast<uint16_t*>(p.kv.blocks) +
+                                    ((2 * (size_t)p.layer + is_v) * plane + (size_t)row * hkv + (h - hq - (is_v ? hkv : 0))) * d;
+          *reinterpret_cast<u32x4_t*>(to + first) = o;
+        } else {
+          // the chunks of a run are neighbouring lanes, all of which are here
+          float a = largest8(x);
+          for (int k = 1; k < lanes; k <<= 1) a = fmaxf(a, __shfl_xor(a, k));
+          const float s = a / 448.0f;
+          const size_t head_row = (2 * (size_t)p.layer + is_v) * plane + (size_t)row * hkv + (h - hq - (is_v ? hkv : 0));
+          uint32_t w[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool in = PAIRS == PAIRS_APART || first + i < 2 * half;
-          x[i] = in ? __builtin_fmaf(x[i], cs[i], y[i] * sn[i]) : x[i];
+          for (int g = 0; g < 2; ++g) {
+            uint32_t v = __builtin_amdgcn_cvt_pk_fp8_f32(code_value(x[4 * g], s), code_value(x[4 * g + 1], s), 0, false);
+            w[g] = __builtin_amdgcn_cvt_pk_fp8_f32(code_value(x[4 * g + 2], s), code_value(x[4 * g + 3], s), v, true);
+          }
+          *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.kv.blocks) + head_row * d + first) = u32x2_t{w[0], w[1]};
+          if ((c & (lanes - 1)) == 0) p.kv.scales[head_row * runs + first / p.kv.gran] = s;
         }
-      }
-      if (is_q || !FP8) {
-        const u32x4_t o = {f2bf2_rn(x[0], x[1]), f2bf2_rn(x[2], x[3]), f2bf2_rn(x[4], x[5]), f2bf2_rn(x[6], x[7])};
-        uint16_t* to = is_q ? p.q_out + ((size_t)r * hq + h) * d
-                            : static_cast<uint16_t*>(p.kv.blocks) +
-                                  ((2 * (size_t)p.layer + is_v) * plane + (size_t)row * hkv + (h - hq - (is_v ? hkv : 0))) * d;
-        *reinterpret_cast<u32x4_t*>(to + first) = o;
-      } else {
-        // the chunks of a run are neighbouring lanes, all of which are here
-        float a = largest8(x);
-        for (int k = 1; k < lanes; k <<= 1) a = fmaxf(a, __shfl_xor(a, k));
-        const float s = a / 448.0f;
-        const size_t head_row = (2 * (size_t)p.layer + is_v) * plane + (size_t)row * hkv + (h - hq - (is_v ? hkv : 0));
-        uint32_t w[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint32_t v = __builtin_amdgcn_cvt_pk_fp8_f32(code_value(x[4 * g], s), code_value(x[4 * g + 1], s), 0, false);
-          w[g] = __builtin_amdgcn_cvt_pk_fp8_f32(code_value(x[4 * g + 2], s), code_value(x[4 * g + 3], s), v, true);
-        }
-        *reinterpret_cast<u32x2_t*>(static_cast<uint8_t*>(p.kv.blocks) + head_row * d + first) = u32x2_t{w[0], w[1]};
-        if ((c & (lanes - 1)) == 0) p.kv.scales[head_row * runs + first / p.kv.gran] = s;
       }
     }
   }
@@ -167,7 +187,7 @@ __global__ __launch_bounds__(RT) void rope_paged_kernel(RopeArgs p, int tokens) 
 hipError_t launch_rope_paged(const RopeArgs& args, hipStream_t stream) {
   RopeArgs p = args;
   divide_pages(p.kv);
-  // a wave per token finds its place: four tokens per workgroup, one where that leaves CUs idle
+  // two tokens per workgroup, one where that leaves CUs idle
   const int tokens = p.T >= 4LL * RTOK * p.num_cus ? RTOK : 1;
   const long long grid = (p.T + tokens - 1) / tokens;
   const int pairs = p.interleaved ? PAIRS_SIDE : p.half % 8 == 0 ? PAIRS_APART : PAIRS_ODD;
