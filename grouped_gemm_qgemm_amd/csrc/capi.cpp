@@ -1,6 +1,7 @@
 // C ABI entry points: host-side argument checks, launch-shape choice and
 // launch. Every check runs before the first HIP call, so a rejected call
 // enqueues nothing and touches no output.
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -428,6 +429,11 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
   return launch_status(qg::launch_tables_ragged(p, stream));
 }
 
+static bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
+  return a_bytes > 0 && b_bytes > 0 && x < y + b_bytes && y < x + a_bytes;
+}
+
 qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* result, const qg_tensor* page_table,
                                const qg_tensor* held_lengths, const qg_tensor* kept_lengths,
                                const qg_tensor* free_count, int32_t page_size, hipStream_t stream) {
@@ -443,6 +449,7 @@ qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* res
   if (kept_lengths->shape[0] != B || page_table->shape[0] != B) return QG_ERR_SHAPE;
   if (result->shape[0] != 2 || free_count->shape[0] != 1) return QG_ERR_SHAPE;
   if (page_size <= 0) return QG_ERR_INVALID_ARG;
+  if (overlap(result->data, 8, free_count->data, 4)) return QG_ERR_INVALID_ARG;
   if (B > qg::kTablesMaxBatch || W >= INT32_MAX / page_size || F > INT32_MAX) return QG_ERR_UNSUPPORTED;
   if (B == 0) return QG_OK;
   qg::ReleaseArgs p{static_cast<uint32_t*>(free_pages->data), static_cast<uint32_t*>(result->data),
@@ -524,6 +531,12 @@ qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg
   if (!std::isfinite(amplitude)) return QG_ERR_INVALID_ARG;
   if (D > 1024 || T > kMostRows || Hq > (1 << 26) / (D > 0 ? D : 1)) return QG_ERR_UNSUPPORTED;
   if (T == 0 || B == 0 || D == 0 || (Hq == 0 && (!k || Hkv == 0))) return QG_OK;
+  // a workgroup's threads read what others of it turn: not in place
+  auto bytes = [&](int64_t H, int64_t stride) { return H > 0 ? 2 * ((T - 1) * std::min<int64_t>(stride, 1ll << 36) + H * D) : 0; };
+  if (q && (overlap(q_out->data, bytes(Hq, Hq * D), q->data, bytes(Hq, qs)) ||
+            (k && (overlap(q_out->data, bytes(Hq, Hq * D), k->data, bytes(Hkv, ks)) ||
+                   overlap(q_out->data, bytes(Hq, Hq * D), v->data, bytes(Hkv, vs))))))
+    return QG_ERR_INVALID_ARG;
   qg::RopeArgs p{};
   if ((st = cache_args(kv, B, true, &p.kv)) != QG_OK) return st;
   if (q && Hq > 0) {

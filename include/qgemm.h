@@ -422,7 +422,8 @@ qg_status tables_ragged_paged(const qg_tensor* input_row_offsets, const qg_tenso
  *   page_table        u32 [B, W]   read only: released entries keep their (stale) content
  *   held_lengths, kept_lengths u32 [B]
  *   free_count        u32 [1]      pages on the stack (result[0] of an earlier call may be it:
- *                                  a view of its first element, in another buffer)
+ *                                  a view of its first element, in another buffer;
+ *                                  QG_ERR_INVALID_ARG where it lies in this call's result)
  *
  * result[1] is 0, or the OR of
  *   1  the stack has no room for the pages (or free_count[0] > F)
@@ -469,7 +470,8 @@ qg_status release_ragged_paged(const qg_tensor* free_pages, const qg_tensor* res
  *
  * D is a multiple of 8 (QG_ERR_ALIGN), at most 1024, and T at most 2^24 (QG_ERR_UNSUPPORTED). One
  * of q and k at least is given (QG_ERR_NULL). Offsets, lengths and page ids are not re-validated on
- * the device; two tokens must not address one slot. q_out must not overlap q.
+ * the device; two tokens must not address one slot. q_out must not overlap the memory
+ * from the first to the last element of q, k or v (QG_ERR_INVALID_ARG).
  */
 qg_status rope_ragged_paged(const qg_tensor* q_out, const qg_tensor* q, const qg_tensor* k, const qg_tensor* v,
                             const int64_t* row_strides_host, const qg_tensor* input_row_offsets,

@@ -291,3 +291,31 @@ def test_more_rows_than_a_launch_has(lib):
     assert read(lib, bb, k=rows(n, (1, 2, 64), QG.BF16), v=rows(n, (1, 2, 64), QG.BF16)) == QG.ERR_UNSUPPORTED
     n = 2**22 + 1
     assert keep(lib, bb, path=rows(n, (1, 4), QG.I32), kept=rows(n, (1,), QG.U32)) == QG.ERR_UNSUPPORTED
+
+
+def test_outputs_over_inputs_are_refused(lib):
+    """A program that turns its queries in place, or has a step's result overwrite the count it reads."""
+    bb = Buf()
+
+    def rows(t, first, shape):
+        """[T, H, D] from element `first` of the buffer of t on."""
+        r = bb.t((1,), QG.BF16)
+        r.data, r.rank = t.data + 2 * first, 3
+        for i, s in enumerate(shape):
+            r.shape[i] = s
+        return r
+
+    fused = bb.t((5 * 8 * 64,), QG.BF16)
+    q, k, v = rows(fused, 0, (3, 4, 64)), rows(fused, 4 * 64, (3, 2, 64)), rows(fused, 6 * 64, (3, 2, 64))
+    no = QG.ERR_INVALID_ARG
+    parts = dict(q=q, k=k, v=v, strides=(512, 512, 512))
+    assert rope(lib, bb, q_out=q, **parts) == no
+    assert rope(lib, bb, q_out=rows(fused, 512 * 3 - 64 - 8, (3, 4, 64)), **parts) == no   # v's last row
+    q = bb.t((3, 4, 64), QG.BF16)
+    assert rope(lib, bb, q=q, q_out=q) == no
+    assert rope(lib, bb, q=q, q_out=q, k=None, v=None) == no
+    assert rope(lib, bb, q_out=rows(fused, 0, (3, 4, 64)), k=rows(fused, 3 * 256 - 8, (3, 2, 64))) == no
+    result = bb.t((2,), QG.U32)
+    count = bb.t((1,), QG.U32)
+    count.data = result.data
+    assert release(lib, bb, result=result, count=count) == no
