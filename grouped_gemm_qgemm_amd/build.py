@@ -36,7 +36,7 @@ COMMON = [
 # arguments preloaded into SGPRs by the dispatcher instead of loading them from
 # the kernel-argument segment at the start of every wave (about 0.25 us per
 # launch); the long kernels gain nothing measurable from it.
-# The attention kernels for few rows call their repeat pass, which is hardly ever
+# The attention kernels for few rows, and those for trees, call their repeat pass, which is hardly ever
 # taken, out of line. With register allocation across calls, what the callee uses
 # decides what is left for the caller's loop: the registers that hold its spilled
 # scalars went to scratch memory there (drafts on e4m3 heads of 128: 106 -> 160 us).

@@ -11,8 +11,8 @@
 // and reads the partner chunk as well where pairs are R / 2 apart: from the cache line that
 // another lane of its wave asked for anyway.
 //
-// 33000 tokens of 48 heads into e4m3 take 160 us, 5.2 TB/s read + written (a large copy:
-// 5.1 to 5.4), eight prompts (4300 tokens, bf16) 17.7 us, 64 tokens 5.4 us on the GPU. A thread
+// 36900 tokens of 48 heads into e4m3 take 160 us, 5.2 TB/s read + written (a large copy:
+// 5.1 to 5.4), eight prompts (3445 tokens, bf16) 17.7 us, 64 tokens 5.4 us on the GPU. A thread
 // with the loads of one head in flight takes 167 us for the first of these, of two 173, of
 // four 163; four tokens per workgroup take 162 us.
 //
