@@ -359,3 +359,19 @@ def test_refusals_with_device_tensors(lib, gpu):
         with pytest.raises(ValueError):
             call(lib, c, {**dev, **over}, out)
     assert (out == 0).all() and np.array_equal(host16(dev["blocks"]), before)
+
+
+@pytest.mark.parametrize("heads,d,gran", [((1, 1), 32, 0), ((1, 1), 32, 32), ((3, 1), 64, 64), ((2, 2), 256, 128), ((20, 2), 128, 0), ((44, 2), 128, 64),
+                                          ((1, 1), 1024, 0), ((5, 1), 72, 0)])
+@pytest.mark.parametrize("rot", [None, 0, 20])
+@pytest.mark.parametrize("kind", ["short", "empty", "long"])
+def test_workgroups_of_many_tokens(lib, gpu, heads, d, gran, rot, kind):
+    """Few heads: a workgroup has up to 16 tokens, of as many sequences (with empty ones between), or of one."""
+    rng = np.random.default_rng(9)
+    if kind == "long":
+        new = [9000, 0, 7001, 1]
+    else:
+        new = rng.integers(0, 9, 5000) if kind == "short" else np.where(rng.random(8000) < 0.3, rng.integers(1, 15, 8000), 0)
+    cut = 5 if heads[0] >= 20 or d == 1024 else 1   # of a few MB of rows
+    new = np.asarray(new)[::cut] if kind != "long" else [n // cut for n in new]
+    check(lib, Case(10, new, rng.integers(0, 50, len(new)), hq=heads[0], hkv=heads[1], d=d, gran=gran, rot=rot, layers=1, spare=5))
