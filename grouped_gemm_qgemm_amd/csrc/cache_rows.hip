@@ -3,9 +3,11 @@
 //
 // Both are copies, bound by HBM, or by latency where they are small. Reading 379000 positions
 // of 8 heads of 128 out of an e4m3 cache as bf16 (2.4 GB read and written) takes 456 us, 5.2
-// TB/s, which is a large copy's rate; 1900 rows of a bf16 cache (16 MB) 6.2 us on the GPU.
+// TB/s, which is a large copy's rate; 1900 rows of a bf16 cache (16 MB) 6 us on the GPU.
 // Three of eight tokens in 32 layers (0.5 MB) move in 3.5 us, paths of 64 sequences in an e4m3
 // cache (39 MB) in 7.6 us: the lengths, the path, the page numbers and the rows in turn.
+#include <algorithm>
+
 #include "paged_common.h"
 
 namespace qg {
@@ -13,7 +15,7 @@ namespace qg {
 namespace {
 
 constexpr int CT = 256;          // threads
-constexpr int CROWS = 16;        // rows per workgroup of a read
+constexpr int CROWS = 64;        // rows per workgroup of a read, at most (a lane each to find them)
 constexpr int CMOVES = 64;       // moves whose rows are found at a time
 constexpr int CBATCH = 8;        // rows in flight per thread
 
@@ -33,19 +35,19 @@ __device__ __forceinline__ void decode8(u32x2_t w, float s, float (&x)[8]) {
 
 }  // namespace
 
-// A workgroup takes CROWS rows of one plane: one wave finds where they lie, then all copy
+// A workgroup takes some rows of one plane: one wave finds where they lie, then all copy
 // chunks of 8 elements.
 template <bool FP8, bool F32>
-__global__ __launch_bounds__(CT) void kv_read_kernel(KvReadArgs p, int planes) {
+__global__ __launch_bounds__(CT) void kv_read_kernel(KvReadArgs p, int planes, int rows_per_wg) {
   __shared__ long long s_row[CROWS];
   const int tid = threadIdx.x, lane = tid & 63;
   const int plane = planes == 2 ? blockIdx.x & 1 : p.out[0] ? 0 : 1;
-  const long long r0 = (long long)(planes == 2 ? blockIdx.x >> 1 : blockIdx.x) * CROWS;
+  const long long r0 = (long long)(planes == 2 ? blockIdx.x >> 1 : blockIdx.x) * rows_per_wg;
   if (tid < 64) {
     const uint32_t rows = p.offs[p.kv.batch];
     int b = owner_of(p.offs, p.kv.batch, (uint32_t)r0);
     const long long r = r0 + lane;
-    if (lane < CROWS) {
+    if (lane < rows_per_wg) {
       long long row = -1;
       if (b >= 0 && r < rows) {
         if (p.offs[b + 1] <= (uint32_t)r) {   // behind the first row's sequence
@@ -63,7 +65,7 @@ __global__ __launch_bounds__(CT) void kv_read_kernel(KvReadArgs p, int planes) {
   __syncthreads();
   const int width = p.kv.hkv * p.kv.d, ch = width >> 3;   // elements and chunks of a row
   const size_t base = (2 * (size_t)p.layer + plane) * p.kv.pages * p.kv.page_size;
-  for (int e = tid; e < CROWS * ch; e += CT) {
+  for (int e = tid; e < rows_per_wg * ch; e += CT) {
     const int i = e / ch, c = e - i * ch;
     const long long row = s_row[i];
     if (row < 0) continue;
@@ -160,13 +162,20 @@ hipError_t launch_kv_read(const KvReadArgs& args, hipStream_t stream) {
   KvReadArgs p = args;
   divide_pages(p.kv);
   const int planes = (p.out[0] ? 1 : 0) + (p.out[1] ? 1 : 0);
-  const unsigned grid = (unsigned)((p.T + CROWS - 1) / CROWS * planes);
+  const int ch = p.kv.hkv * p.kv.d >> 3;
+  // Eight chunks of codes per thread, or four of values, and two workgroups per CU. With 16 rows always,
+  // 465000 rows of one head of 128 took 113 us out of e4m3 (now 79) and 106 out of bf16 (95), 483 of
+  // 16 heads of 256 17 (8).
+  const long long most = std::min<long long>(CROWS, p.T * planes / (2 * p.num_cus));
+  const long long want = std::max<long long>(1, std::min<long long>(most, (p.kv.fp8 ? 8 : 4) * CT / ch));
+  const int rows = (int)std::max<long long>(want, p.T * planes >> 23);   // (a launch has less than 2^32 threads)
+  const unsigned grid = (unsigned)((p.T + rows - 1) / rows * planes);
   if (p.kv.fp8) {
-    if (p.f32) kv_read_kernel<true, true><<<grid, CT, 0, stream>>>(p, planes);
-    else kv_read_kernel<true, false><<<grid, CT, 0, stream>>>(p, planes);
+    if (p.f32) kv_read_kernel<true, true><<<grid, CT, 0, stream>>>(p, planes, rows);
+    else kv_read_kernel<true, false><<<grid, CT, 0, stream>>>(p, planes, rows);
   } else {
-    if (p.f32) kv_read_kernel<false, true><<<grid, CT, 0, stream>>>(p, planes);
-    else kv_read_kernel<false, false><<<grid, CT, 0, stream>>>(p, planes);
+    if (p.f32) kv_read_kernel<false, true><<<grid, CT, 0, stream>>>(p, planes, rows);
+    else kv_read_kernel<false, false><<<grid, CT, 0, stream>>>(p, planes, rows);
   }
   return hipGetLastError();
 }

@@ -253,3 +253,15 @@ def test_refusals_with_device_tensors(lib, gpu):
     with pytest.raises(lib.QgError):
         lib.kv_read_ragged_paged(k, None, offs, None, blocks, table, 2)
     assert np.array_equal(host16(blocks), d.blocks) and (k == 7).all()
+
+
+@pytest.mark.parametrize("hkv,dim,gran", [(1, 8, 0), (1, 32, 32), (1, 128, 0), (2, 128, 128), (4, 72, 0), (16, 256, 0), (16, 256, 64), (3, 1024, 0)])
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32])
+def test_read_in_workgroups_of_few_and_of_many_rows(lib, gpu, hkv, dim, gran, kind):
+    """Up to 64 rows of a workgroup, of as many sequences (with empty ones between), or of one."""
+    rng = np.random.default_rng(3)
+    new = np.where(rng.random(2000) < 0.5, rng.integers(0, 40, 2000), 0) if hkv * dim <= 512 else rng.integers(0, 4, 120)
+    for counts in (new, np.array([int(new.sum()), 0, 1])):
+        history = rng.integers(0, 30, len(counts))
+        d = synth.attention_inputs(21, counts, history, hq=hkv, hkv=hkv, d=dim, page=16, gran=gran, layers=1)
+        check_read(lib, d, counts, rng.integers(0, history + 1), kind=kind)
