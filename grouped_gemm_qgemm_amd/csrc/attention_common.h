@@ -304,7 +304,7 @@ __device__ __forceinline__ AttnItem attn_locate(const AttnArgs& p, int want, Att
 struct AttnTile {
   int r_first, r_count;   // rows of the sequence (token-major)
   int t_first, t_last;    // their tokens
-  int begin, end;         // positions that some row sees: [begin, end)
+  int begin, end;         // positions that some row sees: [begin, end); of a tree, lie within (see tree_narrow)
   int start;              // begin rounded down
 };
 
@@ -569,6 +569,68 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& p, AttnShare& s, int t
     s.cached = (int)p.cache_len[s.b];
   }
   return true;
+}
+
+// What the rows of a tree's tile see lies in [begin, end): none of the history before `begin`, no
+// drafted token from position `end` on; nothing at all where the two are equal. Every wave reads the
+// mask for itself: a lane per token, words in turn.
+struct TreeRange {
+  int begin, end;
+};
+__device__ __forceinline__ TreeRange tree_range(const AttnArgs& p, const AttnItem& it, const AttnTile& t) {
+  const int n = tree_named(p, it.fresh);
+  int low = it.cached, top = 0;
+  for (int tok = t.t_first + (int)(threadIdx.x & 63); tok <= t.t_last; tok += 64) {
+    const uint32_t* words = p.tree + (size_t)(it.row0 + tok) * p.tree_words;
+    int seen = 0;
+#pragma unroll 4
+    for (int w = 0; 32 * w < n; ++w) {
+      const uint32_t x = words[w] & low_bits(n - 32 * w);
+      seen += __popc(x);
+      top = x ? 32 * w + 32 - __clz((int)x) : top;
+    }
+    low = min(low, p.window ? max(0, it.cached - max(p.window - seen, 0)) : 0);
+  }
+#pragma unroll
+  for (int k = 32; k >= 1; k >>= 1) {
+    low = min(low, __shfl_xor(low, k));
+    top = max(top, __shfl_xor(top, k));
+  }
+  low = __builtin_amdgcn_readfirstlane(low);
+  return TreeRange{low, it.cached + __builtin_amdgcn_readfirstlane(top)};
+}
+
+// A part of a tree's tile without the positions at its ends that no row sees: their pages need not
+// exist. False where that leaves none.
+__device__ __forceinline__ bool tree_narrow(const AttnArgs& p, const AttnItem& it, AttnTile& t, AttnPart& part) {
+  if (p.window || part.end > it.cached) {   // (without a window, every row sees all of the history)
+    const TreeRange seen = tree_range(p, it, t);
+    t.begin = seen.begin;
+    part.first = max(part.first, t.begin & ~31);
+    part.end = min(part.end, seen.end);
+  }
+  return max(part.first, t.begin) < part.end;
+}
+
+// Rows of `heads` heads from h on that see nothing of a part: zeros, or (slot >= 0) a part without weight.
+template <int NT, int DP>
+__device__ __forceinline__ void store_unseen(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int heads, int slot) {
+  for (int e = threadIdx.x; e < heads * t.r_count * (DP / 4); e += NT) {
+    const int sub = e / (t.r_count * (DP / 4)), r = e / (DP / 4) % t.r_count, d = e % (DP / 4) * 4;
+    if (slot < 0) {
+      const int row = t.r_first + r, token = over_group(p, row);
+      if (d < p.d)
+        *reinterpret_cast<u32x2_t*>(p.out + ((size_t)(it.row0 + token) * p.hq + (h + sub) * p.group + row - token * p.group) * p.d + d) =
+            u32x2_t{0, 0};
+    } else {
+      float* ws = p.workspace + attn_header_floats(p.target) + (size_t)(slot + sub) * attn_slot_floats(p.bm, DP);
+      *reinterpret_cast<float4_t*>(ws + (size_t)r * DP + d) = float4_t{0.f, 0.f, 0.f, 0.f};
+      if (d == 0) {
+        ws[(size_t)p.bm * DP + 2 * r] = -INFINITY;
+        ws[(size_t)p.bm * DP + 2 * r + 1] = 0.f;
+      }
+    }
+  }
 }
 
 // four e4m3 codes -> four bf16 (exact)

@@ -64,8 +64,8 @@ struct AttnRowsLds {
 // zero; with it: as `rep`, the state of this lane's rows in this wave, says), for the
 // whole workgroup, and then has written nothing.
 template <int DP, int GRAN, int MT, int NW, int NST, bool SAFE, bool TREE>
-__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, int h0, int hw, int c_first, int c_end, int slot,
-                                            AttnRowsLds<DP, GRAN, MT, NW, NST>& lds, AttnRepeat (&rep)[MT]) {
+__device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h0, int hw, int c_first,
+                                            int c_end, int slot, AttnRowsLds<DP, GRAN, MT, NW, NST>& lds, AttnRepeat (&rep)[MT]) {
   constexpr bool FP8 = GRAN > 0;
   constexpr int ES = FP8 ? 1 : 2;              // bytes per cached element
   constexpr int CH = DP * ES / 16;             // chunks per LDS row
@@ -88,7 +88,6 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, j = lane >> 4;
   const int h = h0 + wave % hw, phase = wave / hw, phases = NW / hw;   // this wave's head and blocks
-  const AttnTile t = attn_tile<TREE>(p, it);
 
   // rows of this lane, one per 16-row tile
   const int rows = it.fresh * p.group;
@@ -523,9 +522,12 @@ template <int DP, int GRAN, int MT, int NW, int NST, bool TREE>
 __device__ __attribute__((noinline)) void attend_rows_safe(kernarg_t args, AttnItem it, int h, int hw, int c_first, int c_end,
                                                            int slot, AttnRowsLds<DP, GRAN, MT, NW, NST>* lds) {
   const AttnArgs p = reload_args(args);
+  const AttnItem item = uniform(it);
+  AttnTile t = attn_tile<TREE>(p, item);
+  if (TREE && p.window) t.begin = tree_range(p, item, t).begin;
   AttnRepeat rep[MT];
   for (int pass = 0; pass < kRepeats; ++pass)
-    if (!attend_rows<DP, GRAN, MT, NW, NST, true, TREE>(p, uniform(it), __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(hw),
+    if (!attend_rows<DP, GRAN, MT, NW, NST, true, TREE>(p, item, t, __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(hw),
                                                   __builtin_amdgcn_readfirstlane(c_first), __builtin_amdgcn_readfirstlane(c_end),
                                                   __builtin_amdgcn_readfirstlane(slot), *lds, rep))
       return;
@@ -553,11 +555,13 @@ __global__ __launch_bounds__(NW * 64, (attn_waves<AttnRowsLds<DP, GRAN, MT, NW, 
     it.row0 = s.row0;
     it.fresh = s.fresh;
     it.cached = s.cached;
-    const AttnTile t = attn_tile<TREE>(p, it);
-    const AttnPart part = attn_part<TREE>(p, s, t);
+    AttnTile t = attn_tile<TREE>(p, it);
+    AttnPart part = attn_part<TREE>(p, s, t);
     if (part.first < part.end) {
       AttnRepeat none[MT];
-      if (attend_rows<DP, GRAN, MT, NW, NST, false, TREE>(p, it, s.h, s.hw, part.first, part.end, part.slot, lds, none))
+      if (TREE && !tree_narrow(p, it, t, part))
+        store_unseen<NW * 64, DP>(p, it, t, s.h, s.hw, part.slot);
+      else if (attend_rows<DP, GRAN, MT, NW, NST, false, TREE>(p, it, t, s.h, s.hw, part.first, part.end, part.slot, lds, none))
         attend_rows_safe<DP, GRAN, MT, NW, NST, TREE>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, s.hw, part.first,
                                                       part.end, part.slot, &lds);
     }

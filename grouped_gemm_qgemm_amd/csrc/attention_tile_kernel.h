@@ -549,7 +549,8 @@ __device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnI
                                                            AttnTileLds<DP, GRAN, AW, KB>* lds) {
   const AttnArgs p = reload_args(args);
   const AttnItem item = uniform(it);
-  const AttnTile t = attn_tile<TREE>(p, item);
+  AttnTile t = attn_tile<TREE>(p, item);
+  if (TREE && p.window) t.begin = tree_range(p, item, t).begin;
   AttnRepeat rep;
   for (int pass = 0; pass < kRepeats; ++pass)
     if (!attend_tile<DP, GRAN, AW, KB, true, TREE>(p, item, t, __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(c_first),

@@ -458,10 +458,12 @@ __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tree_kern
     it.row0 = s.row0;
     it.fresh = s.fresh;
     it.cached = s.cached;
-    const AttnTile t = attn_tile<true>(p, it);
-    const AttnPart part = attn_part<true>(p, s, t);
+    AttnTile t = attn_tile<true>(p, it);
+    AttnPart part = attn_part<true>(p, s, t);
     if (part.first < part.end) {
-      if (attend_tree<DP, GRAN, AW, ODD>(p, it, t, s.h, part.first, part.end, part.slot, lds))
+      if (!tree_narrow(p, it, t, part))
+        store_unseen<AW * 64, DP>(p, it, t, s.h, 1, part.slot);
+      else if (attend_tree<DP, GRAN, AW, ODD>(p, it, t, s.h, part.first, part.end, part.slot, lds))
         attend_tile_safe<DP, GRAN, AW, AttnTreeLds<DP, GRAN, AW, ODD>::KB, true>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, part.first, part.end, part.slot, &lds.safe);
     }
     if (!attn_next(p, s, part.take)) return;

@@ -576,6 +576,9 @@ qg_status attention_ragged_paged(const qg_tensor* out, const qg_tensor* q, const
  * tokens i (at position cache_lengths[b] + i) that its row of tree_mask names: bit i % 32 of
  * tree_mask[input_row_offsets[b] + j][i / 32], for i < min(n_b, 32 W). In a tree these are its
  * ancestors and itself. A row that sees nothing (no history, no bit) becomes zeros.
+ * For the rule on pages that are not read, drafted tokens before the last one that some
+ * token of the sequence names count as seen, with the history between the first
+ * position that some token sees and them.
  *
  *   tree_mask  u32 [T, W], W >= 1 (QG_ERR_SHAPE otherwise); bits from n_b on are ignored
  *   window     0, or the number of positions a token sees: the drafted ones that the mask names
