@@ -44,7 +44,7 @@ __global__ __launch_bounds__(CT) void kv_read_kernel(KvReadArgs p, int planes, i
   const int plane = planes == 2 ? blockIdx.x & 1 : p.out[0] ? 0 : 1;
   const long long r0 = (long long)(planes == 2 ? blockIdx.x >> 1 : blockIdx.x) * rows_per_wg;
   if (tid < 64) {
-    const uint32_t rows = p.offs[p.kv.batch];
+    const uint32_t rows = min(p.offs[p.kv.batch], (uint32_t)p.T);   // (offsets are not checked: no row behind the outputs)
     int b = owner_of(p.offs, p.kv.batch, (uint32_t)r0);
     const long long r = r0 + lane;
     if (lane < rows_per_wg) {
