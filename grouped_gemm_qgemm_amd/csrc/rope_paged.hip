@@ -45,7 +45,7 @@ __device__ __forceinline__ float part_of_turn(double t, double f) {
   return (float)((n - rint(n)) + n_rest);
 }
 
-// what the calculation of codes divides by; NaN elements do not count
+// largest magnitude, of which a scale is made; NaN elements do not count
 __device__ __forceinline__ float largest8(const float (&x)[8]) {
   float a = 0.f;
 #pragma unroll
@@ -53,9 +53,10 @@ __device__ __forceinline__ float largest8(const float (&x)[8]) {
   return a;
 }
 
-// e4m3(x / s), nearest even; x / s may pass 448 where s is subnormal and was rounded
+// e4m3(x / s), nearest even; x / s may pass 448 where s is subnormal and was rounded. NaN's code is
+// NaN, also where a run has no other elements but zeros, and the scale 0.
 __device__ __forceinline__ float code_value(float x, float s) {
-  const float v = s > 0.f ? x / s : 0.f;
+  const float v = s > 0.f ? x / s : x == x ? 0.f : x;
   return fabsf(v) > 448.f ? copysignf(448.f, v) : v;
 }
 
