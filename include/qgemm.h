@@ -290,7 +290,8 @@ qg_status grouped_gemm_w4_epilogue(const qg_tensor* c, const qg_tensor* a, const
  *     `scales`; the stored code q stands for q * s. A writer sets
  *     s = amax / 448 (amax: the largest |x| of the run, in fp32) and
  *     q = e4m3(x / s) rounded to nearest even (q = 0 when amax = 0); G is 32, 64
- *     or 128 and divides D.
+ *     or 128 and divides D. NaN elements do not count in amax and have the code of
+ *     NaN, whatever the scale.
  */
 typedef struct {
   qg_tensor blocks;                /* bf16 or fp8 e4m3 [L, 2, P, S, Hkv, D]: layer, K/V plane

@@ -230,7 +230,7 @@ def kproj_inputs(seed: int = 5, batch: int = 8, max_len: int = 1024, Kh: int = 4
     """K-projection workload. Draw order: lengths, hidden, weight, input scales, page table.
 
     planes = 2 draws [W_k | W_v] (2N columns) for the fused key/value projection.
-    cache = "fp8" gives an e4m3 cache (prior codes 0x7F, a NaN the writers never
+    cache = "fp8" gives an e4m3 cache (prior codes 0x7F, a NaN that finite inputs never
     produce) with float32 scales (prior value -1) per `qgran` head-dim elements.
     hidden = "fp8" stores the same normal draws as e4m3 codes with one float32
     input scale per token per 128 columns (amax / 448 of the block), in place of
