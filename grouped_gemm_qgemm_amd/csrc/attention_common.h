@@ -354,6 +354,13 @@ __device__ __forceinline__ uint32_t tree_sees(const AttnArgs& p, const AttnItem&
   return drafted | history;
 }
 
+// A row of a tree whose weights sum to nothing is zeros where it sees nothing; where it sees positions,
+// all of them with scores of -infinity, it has no softmax: 0 / 0. Wherever parts of a row are joined,
+// the latter has a sum of 1, which counts for nothing beside its reference of -infinity, but tells the two apart.
+__device__ __forceinline__ float seen_sum(float sum, bool seen) { return sum == 0.f && seen ? 1.f : sum; }
+// what its sums are multiplied by; m: reference, sum: as seen_sum says
+__device__ __forceinline__ float tree_factor(float m, float sum) { return sum == 0.f ? 0.f : 1.f / (m > -INFINITY ? sum : 0.f); }
+
 // The line's cut into `pieces` shares: the first `extra` have one unit more than `each`.
 struct AttnCut {
   uint32_t units, pieces, each, extra;

@@ -103,7 +103,12 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int part
     };
     join(std::false_type{});
     if (__any(!(fabsf(o[0]) + fabsf(o[1]) + fabsf(o[2]) + fabsf(o[3]) < INFINITY))) join(std::true_type{});
-    const float inv = p.tree && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
+    float inv = 1.f / sum;
+    if (p.tree && __any(sum == 0.f)) {   // the row sees nothing, or scores of -infinity alone (see seen_sum)
+      bool sees = false;
+      for (int s = lane; s < ns; s += 64) sees |= part_at(s)[ml + 1] != 0.f;
+      inv = __any(sees) ? inv : 0.f;
+    }
     const int row = t.r_first + r, token = over_group(p, row);
     uint16_t* to = p.out + ((size_t)(t.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
     if (phase == 0 && d < p.d)

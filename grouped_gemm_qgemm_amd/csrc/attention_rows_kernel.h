@@ -133,6 +133,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
 
   float4_t acc[MT][ND];
   float m[MT], l[MT];     // reference of the weights' exponents (base 2), this lane's share of their sum
+  uint32_t seen[TREE ? MT : 1] = {};   // in a tree: not 0 where the row has seen a position
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     m[mt] = -INFINITY;
@@ -300,6 +301,7 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
             for (int e = 0; e < 8; ++e)
               sc[mt][e >> 2][e & 3] = vis[mt] >> (16 * (e >> 2) + (e & 3)) & 1 ? sc[mt][e >> 2][e & 3] : -INFINITY;
           }
+          seen[mt] |= vis[mt];
         } else if (masked) {
           // positions lo .. min(hi, s_end - 1), counted from lo
           const uint32_t seen = max(min(hi[mt], s_end - 1) - lo[mt] + 1, 0), first = k0 + 4 * j - lo[mt];
@@ -461,6 +463,11 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
       far |= weights_off(m[mt], l[mt]);
     }
     off |= far;
+    if constexpr (TREE) {
+      uint32_t any = seen[mt] | __shfl_xor(seen[mt], 16);
+      any |= __shfl_xor(any, 32);
+      l[mt] = seen_sum(l[mt], any != 0);
+    }
   }
   off = __any(off);
   if (lane == 0) lds.w_off[wave] = off;
@@ -491,17 +498,20 @@ __device__ __forceinline__ bool attend_rows(const AttnArgs& p, const AttnItem& i
     const float base = top == -INFINITY ? 0.f : top;
     float4_t o = {0.f, 0.f, 0.f, 0.f};
     float sum = 0.f;
+    bool some = false;   // in a tree: whether the row has seen a position
     for (int w = sub; w < NW; w += hw) {
       const float f = __builtin_amdgcn_exp2f(lds.w_m[w][r] - base);
       const float4_t x = *reinterpret_cast<const float4_t*>(reinterpret_cast<const float*>(&ring[w][0][0][0]) + r * OS + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = SAFE && !(fabsf(x[i]) < INFINITY) ? o[i] + x[i] : __builtin_fmaf(x[i], f, o[i]);
       sum = __builtin_fmaf(lds.w_l[w][r], f, sum);
+      some |= lds.w_l[w][r] != 0.f;
     }
+    if (TREE) sum = seen_sum(sum, some);
     if (slot < 0) {
       if (d < p.d) {
         const int row = t.r_first + r, token = over_group(p, row);
-        const float inv = TREE && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
+        const float inv = TREE ? tree_factor(top, sum) : 1.f / sum;
         uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + (h0 + sub) * p.group + row - token * p.group) * p.d + d;
         *reinterpret_cast<u32x2_t*>(to) = u32x2_t{f2bf2_rn(o[0] * inv, o[1] * inv), f2bf2_rn(o[2] * inv, o[3] * inv)};
       }

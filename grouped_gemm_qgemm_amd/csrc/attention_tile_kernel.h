@@ -74,7 +74,7 @@ struct AttnTileLds {
   AttnScan<AW * 64> scan;
 };
 
-// A wave's rows: the result, or (slot >= 0) the part of it with its reference and sum.
+// A wave's rows: the result, or (slot >= 0) the part of it with its reference and sum (of a tree: seen_sum).
 template <int DP, bool TREE>
 __device__ __forceinline__ void store_tile(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int slot,
                                            const float16_t (&acc)[DP / 32], float m, float sum) {
@@ -85,7 +85,7 @@ __device__ __forceinline__ void store_tile(const AttnArgs& p, const AttnItem& it
   const int r = wave * 32 + col;
   if (r >= t.r_count) return;
   if (slot < 0) {
-    const float inv = TREE && sum == 0.f ? 0.f : 1.f / sum;   // (in a tree a row may see nothing)
+    const float inv = TREE ? tree_factor(m, sum) : 1.f / sum;
     const int row = t.r_first + r, token = over_group(p, row);
     uint16_t* to = p.out + ((size_t)(it.row0 + token) * p.hq + h * p.group + row - token * p.group) * p.d;
 #pragma unroll
@@ -182,6 +182,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
   float16_t acc[ND];
   float m = -INFINITY, l = 0.f;   // reference of the weights' exponents (base 2), this lane's share of their sum
   float sum;                      // the row's
+  uint32_t seen = 0;              // in a tree: not 0 where the row has seen a position
   {
 #pragma unroll
     for (int n = 0; n < ND; ++n)
@@ -388,6 +389,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
               for (int e = 0; e < 16; ++e) sc[nb][e] = vis[nb] >> (8 * (e / 4) + e % 4) & 1 ? sc[nb][e] : -INFINITY;
             }
+            seen |= vis[nb];
           }
         } else if (masked) {
           // positions lo .. min(hi, s_end - 1), counted from lo
@@ -539,6 +541,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
     if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
   }
 
+  if (TREE) sum = seen_sum(sum, (seen | __shfl_xor(seen, 32)) != 0);
   store_tile<DP, TREE>(p, it, t, h, slot, acc, SAFE ? rep.reference(m) : m, sum);
   return false;
 }

@@ -119,6 +119,7 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
 
   float16_t acc[ND];
   float m = -INFINITY, l = 0.f;   // reference of the weights' exponents (base 2), this lane's share of their sum
+  uint32_t seen = 0;              // not 0 where the row has seen a position
   // A zero that the compiler does not know for one: it would let the accumulators share it with the
   // upper halves of addresses, and hold those in registers of 16 that it spills at every use.
   float none = 0.f;
@@ -350,7 +351,10 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
           const uint32_t vis = tree_sees(p, it, tok, lo, k0 + 32 * nb, s_end) >> (4 * half);
 #pragma unroll
           for (int e = 0; e < 16; ++e) sc[nb][e] = vis >> (8 * (e / 4) + e % 4) & 1 ? sc[nb][e] : -INFINITY;
+          seen |= vis;
         }
+      } else {
+        seen = 1;
       }
       float mx = -INFINITY;
 #pragma unroll
@@ -441,7 +445,7 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
 #pragma unroll
   for (int w = 0; w < AW; ++w) off |= lds.w_off[w];
   if (uniform(off != 0)) return true;   // a scalar branch: the accumulators are not live across the call behind it
-  store_tile<DP, true>(p, it, t, h, slot, acc, m, sum);
+  store_tile<DP, true>(p, it, t, h, slot, acc, m, seen_sum(sum, (seen | __shfl_xor(seen, 32)) != 0));
   return false;
 }
 
