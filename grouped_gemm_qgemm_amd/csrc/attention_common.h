@@ -578,6 +578,16 @@ __device__ __forceinline__ bool attn_next(const AttnArgs& p, AttnShare& s, int t
   return true;
 }
 
+// the largest of the wave's x
+__device__ __forceinline__ int largest(int x) {
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));   // 7 - lane of 8
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, true));   // 15 - lane of 16
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
+
 // What the rows of a tree's tile see lies in [begin, end): none of the history before `begin`, no
 // drafted token from position `end` on; nothing at all where the two are equal. Every wave reads the
 // mask for itself: a lane per token, words in turn.
@@ -598,13 +608,7 @@ __device__ __forceinline__ TreeRange tree_range(const AttnArgs& p, const AttnIte
     }
     low = min(low, p.window ? max(0, it.cached - max(p.window - seen, 0)) : 0);
   }
-#pragma unroll
-  for (int k = 32; k >= 1; k >>= 1) {
-    low = min(low, __shfl_xor(low, k));
-    top = max(top, __shfl_xor(top, k));
-  }
-  low = __builtin_amdgcn_readfirstlane(low);
-  return TreeRange{low, it.cached + __builtin_amdgcn_readfirstlane(top)};
+  return TreeRange{p.window ? it.cached - largest(it.cached - low) : 0, it.cached + largest(top)};
 }
 
 // A part of a tree's tile without the positions at its ends that no row sees: their pages need not
