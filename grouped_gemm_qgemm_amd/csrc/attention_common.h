@@ -753,9 +753,10 @@ void attention_rows_shape(AttnArgs& p, int mt);
 hipError_t launch_attention_rows(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_rows_tree(const AttnArgs& p, int mt, unsigned grid, hipStream_t stream);
 hipError_t launch_attention_tiles(const AttnArgs& p, unsigned grid, hipStream_t stream);
-// The same for trees with many rows: rows per tile, and workgroups that run at once. tall: tiles
-// of 256 rows where there are such instances, else of 128.
-void attention_tree_shape(AttnArgs& p, bool tall);
-hipError_t launch_attention_tree(const AttnArgs& p, bool tall, unsigned grid, hipStream_t stream);
+// The same for trees with many rows: rows per tile, and workgroups that run at once. Tiles have 128
+// rows: TREE_FEW with the weights' remainders on bf16 caches, TREE_TALL 256 where there are such instances.
+enum TreeTiles { TREE_FEW, TREE_MANY, TREE_TALL };
+void attention_tree_shape(AttnArgs& p, TreeTiles tiles);
+hipError_t launch_attention_tree(const AttnArgs& p, TreeTiles tiles, unsigned grid, hipStream_t stream);
 
 }  // namespace qg

@@ -181,10 +181,11 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   // average too: 256 tokens on 1000 and a chunk of 512 after 8000, bf16 863 us, 281 us as two calls.
   //
   // Trees have a kernel of their own for many rows, which on bf16 caches is the faster one from 17
-  // rows on (32 trees of 6 tokens on 4000: 123 us against 129, 64 of 8 on 1000 54 against 70, heads
-  // of 256 212 against 238), but not with 16 or fewer (32 of 4 on 4000: 121 against 112, heads of 256 212
-  // against 205; heads of 64 57 against 67), and on e4m3 where the other is (32 of 8 on 4000: 110 against
-  // 90; 8 of them 48 against 52; heads of 256, 8 of 8, 117 against 94).
+  // rows on (32 trees of 6 tokens on 4000: 125 us against 129, 64 of 8 on 1000 55 against 70, of heads of
+  // 64 33 against 49, heads of 256, 32 of 6 on 4000, 245 against 241), but not with 16 or fewer (32 of 4 on
+  // 4000, without the remainders below: 121 against 112, heads of 256 212 against 205; heads of 64 57 against
+  // 67), and on e4m3 where the other is (32 of 8 on 4000: 110 against 90; 8 of them 48 against 52; heads of
+  // 256, 8 of 8, 117 against 94).
   const int mt = rows > 16LL * p.batch ? 2 : 1;
   const bool some = (!p.tree || p.fp8) && rows <= 32LL * p.batch && (4LL * p.batch * p.hkv > p.num_cus || (p.fp8 && p.d > 128));
   const bool few = mt == 1 || some;
@@ -209,8 +210,14 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   if (p.tree) {
     // Tiles of 256 rows where 128 are not enough for most sequences: 32 trees of 64 tokens, 4 heads to one,
     // on up to 8191 positions 200 us against 247, 6 of 20 to 120 on up to 40000 (e4m3) 457 against 503.
-    const bool tall = rows > 128LL * p.batch;
-    attention_tree_shape(p, tall);
+    //
+    // Up to 32 rows on bf16 caches: with the weights' remainders, as in the kernel for few rows. The error
+    // against 64 bits is that of the result's rounding then, 1.66e-3 of the result (root mean square), without
+    // them 2.33e-3; 32 trees of 6 on 4000 take 125 us against 122, 64 of 8 on 1000 55 against 53, heads of 64 33.5
+    // against 30, of 256 245 against 211. With more rows they cost more and are left out, as in the other calls:
+    // 32 of 32 on 4000 149 against 145, heads of 64 90 against 78, of 256 285 against 242; 32 of 64 213 against 170.
+    const TreeTiles kind = rows > 128LL * p.batch ? TREE_TALL : rows > 32LL * p.batch ? TREE_MANY : TREE_FEW;
+    attention_tree_shape(p, kind);
     p.target = std::max<int>(std::min<int>(p.target, kTreeRows / p.bm), p.hkv);   // the workspace's slots
     set_shape(p, p.bm, kTileStep);
     const long long tree_tiles = rows / p.bm + p.batch;
@@ -218,7 +225,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
     const long long pieces = std::min<long long>(p.target / p.hkv, tree_tiles * ((room + p.step - 1) / p.step));
     const long long grid = (pieces + 7) / 8 * 8 * p.hkv;
     if (grid > kMostWorkgroups) return hipErrorNotSupported;
-    const hipError_t e = launch_attention_tree(p, tall, (unsigned)grid, stream);
+    const hipError_t e = launch_attention_tree(p, kind, (unsigned)grid, stream);
     return e != hipSuccess || pieces <= 1 ? e : launch_join(p, pieces, stream);
   }
   p.min_chunk = kTileMinChunk;

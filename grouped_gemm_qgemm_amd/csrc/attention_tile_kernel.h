@@ -74,6 +74,18 @@ struct AttnTileLds {
   AttnScan<AW * 64> scan;
 };
 
+// What eight weights lose as the bf16 pairs r.
+__device__ __forceinline__ u32x4_t remainders(const float (&w)[8], u32x4_t r) {
+#pragma clang fp contract(off)   // the same remainder whatever the code around it: not one of an unrounded product
+  u32x4_t rest;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t v = r[g];
+    rest[g] = f2bf2_rn(w[2 * g] - bf2f((uint16_t)v), w[2 * g + 1] - bf2f((uint16_t)(v >> 16)));
+  }
+  return rest;
+}
+
 // A wave's rows: the result, or (slot >= 0) the part of it with its reference and sum (of a tree: seen_sum).
 template <int DP, bool TREE>
 __device__ __forceinline__ void store_tile(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int slot,
@@ -115,8 +127,9 @@ __device__ __forceinline__ void store_tile(const AttnArgs& p, const AttnItem& it
 // that slot of the workspace else. GRAN: head-dim elements per scale of an e4m3 cache, 0
 // for bf16. SAFE: values are selected per token. Returns whether some row has to be computed
 // again (without SAFE: sums are too large, infinities, NaN or zero; with it: as `rep`, the
-// state of this lane's row, says), for the whole workgroup, and then has written nothing.
-template <int DP, int GRAN, int AW, int KB, bool SAFE, bool TREE>
+// state of this lane's row, says), for the whole workgroup, and then has written nothing. REST (bf16): what
+// the weights lose to bf16 is multiplied with the values too.
+template <int DP, int GRAN, int AW, int KB, bool SAFE, bool TREE, bool REST>
 __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int c_first, int c_end,
                                             int slot, AttnTileLds<DP, GRAN, AW, KB>& lds, AttnRepeat& rep) {
   constexpr bool FP8 = GRAN > 0;
@@ -432,8 +445,8 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           }
         l += l_block;
 
-        // weights of 16 positions as the B operand; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
-        auto weights = [&](int nb, int ks, int run) {
+        // weights of 16 positions as the B operand, and REST's of them; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
+        auto weights = [&](int nb, int ks, int run, u32x4_t& rest) {
           float w[8];
           const int key0 = nb * 32 + ks * 16 + 4 * half;
 #pragma unroll
@@ -454,7 +467,9 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
               }
             }
           }
-          return u32x4_t{f2bf2_rn(w[0], w[1]), f2bf2_rn(w[2], w[3]), f2bf2_rn(w[4], w[5]), f2bf2_rn(w[6], w[7])};
+          const u32x4_t r = {f2bf2_rn(w[0], w[1]), f2bf2_rn(w[2], w[3]), f2bf2_rn(w[4], w[5]), f2bf2_rn(w[6], w[7])};
+          if constexpr (REST) rest = remainders(w, r);
+          return r;
         };
         // V^T fragment of strip n: lane m of a 16-lane group names row m / 4 of four and
         // elements 4 (m % 4) .. + 3 of 16, and receives the four rows of column m
@@ -466,13 +481,15 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           return u32x4_t{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
         };
         // SAFE: the product of strip n's values vf with the weights, infinities and NaN apart
-        auto product = [&](u32x4_t vf, u32x4_t pf, int nb, int ks, float16_t sum) {
+        auto product = [&](u32x4_t vf, u32x4_t pf, u32x4_t rest, int nb, int ks, float16_t sum) {
           uint32_t one[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) one[e] = sees >> (16 * nb + 8 * ks + e) & 1 ? 0x3F80u : 0u;
           const u32x4_t of = {one[0] | one[1] << 16, one[2] | one[3] << 16, one[4] | one[5] << 16, one[6] | one[7] << 16};
           const u32x4_t v = finite(vf);
-          return mfma32x32x16_bf16(vf ^ v, of, mfma32x32x16_bf16(v, pf, sum));
+          sum = mfma32x32x16_bf16(v, pf, sum);
+          if constexpr (REST) sum = mfma32x32x16_bf16(v, rest, sum);
+          return mfma32x32x16_bf16(vf ^ v, of, sum);
         };
         if constexpr (FIRST) __builtin_amdgcn_s_setprio(1);
         if (!SAFE || !masked) {
@@ -480,12 +497,12 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-              u32x4_t pf;
+              u32x4_t pf, rest = {};
 #pragma unroll
               for (int n = 0; n < ND; ++n) {
-                if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
+                if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0, rest);
                 const u32x4_t vf = values(nb, ks, n);
-                acc[n] = SAFE ? product(vf, pf, nb, ks, acc[n]) : mfma32x32x16_bf16(vf, pf, acc[n]);
+                acc[n] = SAFE ? product(vf, pf, rest, nb, ks, acc[n]) : mfma32x32x16_bf16(vf, pf, acc[n]);
               }
             }
         } else {
@@ -497,7 +514,8 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 #pragma unroll
               for (int n = 0; n < ND; ++n) {
                 const u32x4_t vf = values(nb, ks, n);
-                const u32x4_t pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
+                u32x4_t rest = {};
+                const u32x4_t pf = weights(nb, ks, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0, rest);
 #pragma unroll 1
                 for (int tt = t.t_first; tt <= t.t_last; ++tt) {
                   const int t_hi = p.causal ? it.cached + tt : it.cached + it.fresh - 1;
@@ -512,7 +530,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
                   }
                   const u32x4_t vs = {vf.x & (keep[0] | keep[1] << 16), vf.y & (keep[2] | keep[3] << 16),
                                       vf.z & (keep[4] | keep[5] << 16), vf.w & (keep[6] | keep[7] << 16)};
-                  const float16_t with = product(vs, pf, nb, ks, acc[n]);
+                  const float16_t with = product(vs, pf, rest, nb, ks, acc[n]);
 #pragma unroll
                   for (int e = 0; e < 16; ++e) acc[n][e] = tt == tok ? with[e] : acc[n][e];
                 }
@@ -547,7 +565,7 @@ __device__ __forceinline__ bool attend_tile(const AttnArgs& p, const AttnItem& i
 }
 
 // Called, not inlined: hardly ever taken, and its registers stay out of the kernel's.
-template <int DP, int GRAN, int AW, int KB, bool TREE>
+template <int DP, int GRAN, int AW, int KB, bool TREE, bool REST>
 __device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnItem it, int h, int c_first, int c_end, int slot,
                                                            AttnTileLds<DP, GRAN, AW, KB>* lds) {
   const AttnArgs p = reload_args(args);
@@ -556,7 +574,7 @@ __device__ __attribute__((noinline)) void attend_tile_safe(kernarg_t args, AttnI
   if (TREE && p.window) t.begin = tree_range(p, item, t).begin;
   AttnRepeat rep;
   for (int pass = 0; pass < kRepeats; ++pass)
-    if (!attend_tile<DP, GRAN, AW, KB, true, TREE>(p, item, t, __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(c_first),
+    if (!attend_tile<DP, GRAN, AW, KB, true, TREE, REST>(p, item, t, __builtin_amdgcn_readfirstlane(h), __builtin_amdgcn_readfirstlane(c_first),
                                                __builtin_amdgcn_readfirstlane(c_end), __builtin_amdgcn_readfirstlane(slot), *lds, rep))
       return;
 }
@@ -580,8 +598,8 @@ __global__ __launch_bounds__(256, DP > 128 ? 1 : 2) void attention_tile_kernel(A
   }
   const int slot = t.end - t.start <= it.chunk ? -1 : it.slots + (it.tile * p.hkv + h) * it.nsplit + it.split;
   AttnRepeat none;
-  if (attend_tile<DP, GRAN, AW, KB, false, false>(p, it, t, h, c_first, c_end, slot, lds, none))
-    attend_tile_safe<DP, GRAN, AW, KB, false>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, h, c_first, c_end, slot, &lds);
+  if (attend_tile<DP, GRAN, AW, KB, false, false, false>(p, it, t, h, c_first, c_end, slot, lds, none))
+    attend_tile_safe<DP, GRAN, AW, KB, false, false>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, h, c_first, c_end, slot, &lds);
 }
 
 }  // namespace qg

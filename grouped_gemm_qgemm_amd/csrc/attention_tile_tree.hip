@@ -7,16 +7,26 @@ namespace {
 
 // f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call.
 template <typename F>
-void with_tree_kernel(const AttnArgs& p, bool tall, F&& f) {
-#define QG_ATTN(DP, GRAN)                                                                                          \
+void with_tree_kernel(const AttnArgs& p, TreeTiles tiles, F&& f) {
+#define QG_ATTN_REST(DP, GRAN, REST)                                                                               \
   do {                                                                                                             \
-    if (odd) f(attention_tree_kernel<DP, GRAN, 4, true>, 4, AttnTreeLds<DP, GRAN, 4, true>::ONE ? 1 : 2);            \
-    else f(attention_tree_kernel<DP, GRAN, 4, false>, 4, AttnTreeLds<DP, GRAN, 4, false>::ONE ? 1 : 2);              \
+    if (odd) f(attention_tree_kernel<DP, GRAN, 4, true, REST>, 4, AttnTreeLds<DP, GRAN, 4, true>::ONE ? 1 : 2);      \
+    else f(attention_tree_kernel<DP, GRAN, 4, false, REST>, 4, AttnTreeLds<DP, GRAN, 4, false>::ONE ? 1 : 2);        \
   } while (0)
-#define QG_ATTN_TALL(GRAN)                                                     \
-  do {                                                                         \
-    if (tall && !odd) f(attention_tree_kernel<128, GRAN, 8, false>, 8, 1);     \
-    else QG_ATTN(128, GRAN);                                                   \
+#define QG_ATTN(DP, GRAN)                                               \
+  do {                                                                  \
+    if constexpr (GRAN == 0) {                                          \
+      if (tiles == TREE_FEW) {                                          \
+        QG_ATTN_REST(DP, GRAN, true);                                   \
+        break;                                                          \
+      }                                                                 \
+    }                                                                   \
+    QG_ATTN_REST(DP, GRAN, false);                                      \
+  } while (0)
+#define QG_ATTN_TALL(GRAN)                                                                    \
+  do {                                                                                        \
+    if (tiles == TREE_TALL && !odd) f(attention_tree_kernel<128, GRAN, 8, false, false>, 8, 1); \
+    else QG_ATTN(128, GRAN);                                                                  \
   } while (0)
   const bool odd = p.page_size % 16 != 0;
   const int gran = p.fp8 ? p.gran : 0;
@@ -35,21 +45,22 @@ void with_tree_kernel(const AttnArgs& p, bool tall, F&& f) {
     else if (gran == 64) QG_ATTN(256, 64);
     else QG_ATTN(256, 128);
   }
+#undef QG_ATTN_REST
 #undef QG_ATTN
 #undef QG_ATTN_TALL
 }
 
 }  // namespace
 
-void attention_tree_shape(AttnArgs& p, bool tall) {
-  with_tree_kernel(p, tall, [&](auto, int nw, int resident) {
+void attention_tree_shape(AttnArgs& p, TreeTiles tiles) {
+  with_tree_kernel(p, tiles, [&](auto, int nw, int resident) {
     p.bm = 32 * nw;
     p.target = p.num_cus * resident;
   });
 }
 
-hipError_t launch_attention_tree(const AttnArgs& p, bool tall, unsigned grid, hipStream_t stream) {
-  with_tree_kernel(p, tall, [&](auto kernel, int nw, int) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
+hipError_t launch_attention_tree(const AttnArgs& p, TreeTiles tiles, unsigned grid, hipStream_t stream) {
+  with_tree_kernel(p, tiles, [&](auto kernel, int nw, int) { kernel<<<grid, nw * 64, 0, stream>>>(p); });
   return hipGetLastError();
 }
 

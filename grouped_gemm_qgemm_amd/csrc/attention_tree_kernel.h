@@ -55,7 +55,10 @@ struct AttnTreeLds {
 
 // Positions [c_first, c_end) of one tile, as attend_tile without SAFE; block by block and sum by
 // sum as it does with it, so that rows which need no repetition come out alike.
-template <int DP, int GRAN, int AW, bool ODD>
+//
+// REST: what the weights lose to bf16 is multiplied with the values too (half as many MFMAs again; which
+// calls have it is the launcher's choice).
+template <int DP, int GRAN, int AW, bool ODD, bool REST>
 __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& it, const AttnTile& t, int h, int c_first, int c_end,
                                             int slot, AttnTreeLds<DP, GRAN, AW, ODD>& lds) {
   typedef AttnTreeLds<DP, GRAN, AW, ODD> Lds;
@@ -255,8 +258,8 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
       return *reinterpret_cast<const float4_t*>(reinterpret_cast<const char*>(&lds.b.scales[0][0]) + x.s_base +
                                                 (((w * 2 + plane) * R + run) * PW + o) * 4);
     };
-    // weights of 16 positions; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
-    auto weights = [&](const Scores& sc, const Place& x, int nb, int ks, int run) {
+    // weights of 16 positions, and REST's of them; key slots 0..3 are key0 + 0..3, 4..7 key0 + 8..11
+    auto weights = [&](const Scores& sc, const Place& x, int nb, int ks, int run, u32x4_t& rest) {
       float w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = sc[nb][8 * ks + e];
@@ -265,7 +268,9 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] *= e < 4 ? v0[e] : v1[e - 4];
       }
-      return u32x4_t{f2bf2_rn(w[0], w[1]), f2bf2_rn(w[2], w[3]), f2bf2_rn(w[4], w[5]), f2bf2_rn(w[6], w[7])};
+      const u32x4_t r = {f2bf2_rn(w[0], w[1]), f2bf2_rn(w[2], w[3]), f2bf2_rn(w[4], w[5]), f2bf2_rn(w[6], w[7])};
+      if constexpr (REST) rest = remainders(w, r);
+      return r;
     };
     // S^T = K Q^T of the block at x
     auto score = [&](Scores& sc, const Place& x) {
@@ -327,15 +332,16 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
         return u32x4_t{(uint32_t)w0, (uint32_t)(w0 >> 32), (uint32_t)w1, (uint32_t)(w1 >> 32)};
       };
       __builtin_amdgcn_s_setprio(1);
-      u32x4_t f[PF], w;
+      u32x4_t f[PF], w, rest;
 #pragma unroll
       for (int j = 0; j < PF; ++j) f[j] = frag(j);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < VS; ++j) {
         const int n = j % ND;
-        if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) w = weights(sc, x, j / (2 * ND), j / ND % 2, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0);
+        if (n == 0 || (FP8 && n * 32 % (FP8 ? GRAN : 1) == 0)) w = weights(sc, x, j / (2 * ND), j / ND % 2, FP8 ? n * 32 / (FP8 ? GRAN : 1) : 0, rest);
         acc[n] = mfma32x32x16_bf16(f[j % PF], w, acc[n]);
+        if constexpr (REST) acc[n] = mfma32x32x16_bf16(f[j % PF], rest, acc[n]);
         if (j + PF < VS) f[j % PF] = frag(j + PF);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -450,7 +456,7 @@ __device__ __forceinline__ bool attend_tree(const AttnArgs& p, const AttnItem& i
 }
 
 // A workgroup per share (see attn_share).
-template <int DP, int GRAN, int AW, bool ODD>
+template <int DP, int GRAN, int AW, bool ODD, bool REST>
 __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tree_kernel(AttnArgs p) {
   __shared__ AttnTreeLds<DP, GRAN, AW, ODD> lds;
   AttnShare s = attn_share<AW * 64, true, 1>(p, lds.share);
@@ -467,8 +473,8 @@ __global__ __launch_bounds__(AW * 64, DP > 128 ? 1 : 2) void attention_tree_kern
     if (part.first < part.end) {
       if (!tree_narrow(p, it, t, part))
         store_unseen<AW * 64, DP>(p, it, t, s.h, 1, part.slot);
-      else if (attend_tree<DP, GRAN, AW, ODD>(p, it, t, s.h, part.first, part.end, part.slot, lds))
-        attend_tile_safe<DP, GRAN, AW, AttnTreeLds<DP, GRAN, AW, ODD>::KB, true>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, part.first, part.end, part.slot, &lds.safe);
+      else if (attend_tree<DP, GRAN, AW, ODD, REST>(p, it, t, s.h, part.first, part.end, part.slot, lds))
+        attend_tile_safe<DP, GRAN, AW, AttnTreeLds<DP, GRAN, AW, ODD>::KB, true, REST>((kernarg_t)__builtin_amdgcn_kernarg_segment_ptr(), it, s.h, part.first, part.end, part.slot, &lds.safe);
     }
     if (!attn_next(p, s, part.take)) return;
     __syncthreads();   // the next part's loads overwrite what the last one's blocks were read from
