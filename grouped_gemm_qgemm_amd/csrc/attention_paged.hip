@@ -39,7 +39,7 @@ constexpr int dp_of(int64_t d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // A wave per row: its lanes take DP / 4 groups of four floats of 256 / DP parts at a
 // time, eight such steps in flight, so that a row of up to 2048 / DP parts costs one
 // memory latency after its record's.
-template <int DP>
+template <int DP, bool TREE>
 __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int parts, int rows_per_wg) {
   constexpr int LR = DP / 4, PH = 64 / LR;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(JT) void attention_join_kernel(AttnArgs p, int part
     join(std::false_type{});
     if (__any(!(fabsf(o[0]) + fabsf(o[1]) + fabsf(o[2]) + fabsf(o[3]) < INFINITY))) join(std::true_type{});
     float inv = 1.f / sum;
-    if (p.tree && __any(sum == 0.f)) {   // the row sees nothing, or scores of -infinity alone (see seen_sum)
+    if (TREE && __any(sum == 0.f)) {   // the row sees nothing, or scores of -infinity alone (see seen_sum)
       bool sees = false;
       for (int s = lane; s < ns; s += 64) sees |= part_at(s)[ml + 1] != 0.f;
       inv = __any(sees) ? inv : 0.f;
@@ -123,9 +123,11 @@ static hipError_t launch_join(const AttnArgs& p, long long cut, hipStream_t stre
   const int per_wg = cut * p.hkv * rows <= 64LL * p.num_cus ? 4 : 16;
   const long long parts = (rows + per_wg - 1) / per_wg;
   const dim3 grid((unsigned)(cut * parts * p.hkv));
-  if (p.d <= 64) attention_join_kernel<64><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
-  else if (p.d <= 128) attention_join_kernel<128><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
-  else attention_join_kernel<256><<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
+  auto join = [&](auto of_64, auto of_128, auto of_256) {
+    (p.d <= 64 ? of_64 : p.d <= 128 ? of_128 : of_256)<<<grid, JT, 0, stream>>>(p, (int)parts, per_wg);
+  };
+  if (p.tree) join(attention_join_kernel<64, true>, attention_join_kernel<128, true>, attention_join_kernel<256, true>);
+  else join(attention_join_kernel<64, false>, attention_join_kernel<128, false>, attention_join_kernel<256, false>);
   return hipGetLastError();
 }
 
