@@ -146,10 +146,10 @@ __device__ __forceinline__ void kproj_store_tile(
         const long long d = row_dst[wm * 48 + mt * 16 + q * 4 + i];
         if (d < 0) continue;
         const float sc = am[mt][i] / 448.0f;   // correctly rounded fp32 division
-        // NaN's code is NaN, also where a run has no other elements but zeros, and the scale 0
-        auto code_value = [&](float x) { return sc > 0.f ? x / sc : x == x ? 0.f : x; };
-        const float v0 = code_value(acc[mt][0][i]), v1 = code_value(acc[mt][1][i]);
-        const int pk = __builtin_amdgcn_cvt_pk_fp8_f32(v0, v1, 0, false);   // nearest even, low half
+        // scale 0: codes 0 without a sign, but NaN's for a NaN
+        const float den = sc > 0.f ? sc : INFINITY;
+        const int pk = __builtin_amdgcn_cvt_pk_fp8_f32(acc[mt][0][i] / den, acc[mt][1][i] / den, 0, false)   // nearest even, low half
+                       & (sc > 0.f ? 0xFFFF : 0x7F7F);
         blocks[d * n_plane + col] = (uint8_t)pk;
         blocks[d * n_plane + col + 16] = (uint8_t)(pk >> 8);
         if (scale_writer) kv_scales[d * nsc + (colp + wn * 32) / qgran] = sc;
