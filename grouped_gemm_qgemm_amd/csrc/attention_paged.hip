@@ -9,7 +9,8 @@
 // It is a second launch on the same stream rather than the task of the last
 // part to finish: that needs counters which every call must find at zero, and
 // ordering between the XCDs' caches within a kernel. It takes 3 to 4 us where nothing or
-// little was cut and 6 to 11 us after a decode step of 64 sequences.
+// little was cut, 6 to 11 us after a decode step of 64 sequences and 17 to 20 where large trees
+// left cut tiles of 256 rows.
 #include <algorithm>
 #include <type_traits>
 
@@ -211,7 +212,7 @@ hipError_t launch_attention_paged(const AttnArgs& args, hipStream_t stream) {
   }
   if (p.tree) {
     // Tiles of 256 rows where 128 are not enough for most sequences: 32 trees of 64 tokens, 4 heads to one,
-    // on up to 8191 positions 200 us against 247, 6 of 20 to 120 on up to 40000 (e4m3) 457 against 503.
+    // on up to 8191 positions 210 us against 244, 6 of 20 to 120 on up to 40000 (e4m3) 459 against 516.
     //
     // Up to 32 rows on bf16 caches: with the weights' remainders, as in the kernel for few rows. The error
     // against 64 bits is that of the result's rounding then, 1.66e-3 of the result (root mean square), without

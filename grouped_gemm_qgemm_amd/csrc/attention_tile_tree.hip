@@ -5,7 +5,12 @@ namespace qg {
 
 namespace {
 
-// f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call.
+// f(kernel, waves per workgroup, workgroups per CU) of the instance that serves a call. Tiles of 256 rows
+// (TREE_TALL) are for heads of 65 to 128 on pages of a multiple of 16: with heads of 64 they lose (32 trees of
+// 64 tokens on 1 to 8191 positions, bf16, 151 us against 145; their e4m3 blocks are too small for eight waves to
+// load), and for heads of 256 LDS has no room for the blocks of 64 positions that eight waves need. On other
+// pages they would win (pages of 20: those trees with heads of 128 218 us against 250, 6 of 20 to 120 on up
+// to 40000, e4m3, 435 against 500), but pages that are no multiple of 16 are not given an instance more.
 template <typename F>
 void with_tree_kernel(const AttnArgs& p, TreeTiles tiles, F&& f) {
 #define QG_ATTN_REST(DP, GRAN, REST)                                                                               \

@@ -12,16 +12,18 @@
 //     there by the lane that loaded them.
 //   * Which drafted tokens a row sees is a word of bits per block; blocks of the history need none.
 //
-// Bound by the MFMAs and the softmax between them. 32 trees of 64 tokens on 1 to 8191 positions
-// (32 heads on 8 of 128, bf16, 139 GFLOP, 585 MB): 180 us and a join of 17 to 20, 770 TFLOP/s;
-// a block of 256 rows on 64 positions takes 1.9 us when its pages are in the caches (1136
-// TFLOP/s, the library's large product: 1373), 2.1 to 2.3 from HBM, and the start and end of a
-// part 8 to 13 us, of which a workgroup has one or two. 6 trees of 20 to 120 on 8000 to 40000
-// (e4m3, runs of 64, 244 GFLOP): 454 us with the join, 536 TFLOP/s; the scales of two runs and the
-// conversion are 210 vector instructions per wave and block beside the 230 of a bf16 cache.
+// What bounds it: within a block the MFMAs and the softmax in turn, over a call the ends of parts. 32
+// trees of 64 tokens on 1 to 8191 positions (32 heads on 8 of 128, bf16, 139 GFLOP, 585 MB) take 208 us
+// with the join of 17 to 20, 670 TFLOP/s. A block of 256 rows on 64 positions takes 1.9 us when its pages
+// are in the caches (1136 TFLOP/s, the library's large product: 1373), 2.1 to 2.3 from HBM, so some 145 us of
+// these are blocks; the start and end of a part take 8 to 13, and a workgroup has one to three of them: over
+// the whole call the MFMAs are busy a third of the time. 6 trees of 20 to 120 on 8000 to 40000 (e4m3, runs of
+// 64, 244 GFLOP): 460 us with the join, 530 TFLOP/s; the scales of two runs and the conversion are 210 vector
+// instructions per wave and block beside the 230 of a bf16 cache, MFMAs busy 23 %, and a tree of more than 64
+// tokens makes a second tile that reads and converts its whole history again.
 // Tried: items of whole tiles and chunks instead of shares (bf16 232 us), two groups of waves that
 // take turns at the MFMAs (204, e4m3 spills), fragments 6 or 8 ahead (level), tiles of 128 rows
-// (247, e4m3 503).
+// (244, e4m3 516, against 210 and 459).
 #pragma once
 
 #include <type_traits>
